@@ -4,9 +4,9 @@ Argument marshalling only: every step of the operation runs in the library's
 HIP kernels.  PyTorch supplies device memory and the current stream.  There is
 no fallback: if the library is not built, or the call fails, this raises.
 
-The C entry points have the same names; see include/topk_transform.h and
-include/indexer_topk.h for the argument meaning, layouts, ownership and error
-behaviour.
+The C entry points have the same names; see include/topk_transform.h,
+include/indexer_topk.h and include/latent_attention.h for the argument meaning,
+layouts, ownership and error behaviour.
 """
 from __future__ import annotations
 
@@ -14,7 +14,11 @@ import ctypes
 import os
 from typing import Optional, Tuple
 
+from . import latent as _latent
 from .build import LIB_PATH
+from .latent import (EXPORTED_LATENT, LATENT_DIM, LATENT_HEAD_DIM, LATENT_ROPE_DIM, AppendPlan, latent_attention,
+                     latent_attention_expanded, latent_attention_paged, latent_cache_load, latent_cache_load_paged,
+                     latent_cache_store, paged_append_plan)
 
 TOPK_MAX_K = 2048
 STREAM_SHAPES = 3   # compiled streaming-kernel shapes: topk_set_stream_shape accepts -1 and 0..STREAM_SHAPES-1
@@ -91,6 +95,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.indexer_set_window_override.restype = ctypes.c_int
     lib.indexer_set_select_mode.argtypes = [c_i32]
     lib.indexer_set_select_mode.restype = ctypes.c_int
+    _latent.declare(lib)
     _lib = lib
     return lib
 

@@ -1,0 +1,591 @@
+// Latent attention, absorbed form, on gfx950: every head of a token reads the
+// same cached rows, so a workgroup stages a tile of rows in LDS once for all
+// its heads, and keys and values are the same bytes.
+//
+//   z[h, j] = scale * (s_j q_c[h] . c_j + q_r[h] . r_j)
+//   out[h]  = sum_j softmax_j(z[h]) s_j c_j          (s_j = 1 in a bf16 cache)
+//
+// One pass over the rows with a running reference maximum and sum per head.
+//
+// Tiling.  A pair of waves owns 32 heads, a workgroup 1, 2 or 4 pairs (up to
+// 128 heads); a tile is 32 keys.  Both products are taken transposed,
+//   S^T = K Q^T   (rows: keys,          columns: heads),
+//   O^T = V^T P^T (rows: latent values, columns: heads),
+// so that a lane keeps one head throughout: its column of S^T, that head's
+// maximum and sum, and its column of O^T.  A lane's 16 scores of a tile are then
+// exactly the elements of P^T that it has to feed to the second product, when
+// the keys of a step are taken in the order the accumulator holds them:
+// weights never leave their registers.  The pair splits a row of the cache:
+// each wave multiplies out half of the 576 values for S^T (the halves are
+// added through LDS, and both waves then hold the same weights) and makes half
+// of O^T's 512 rows.  Its Q (18 x 4 registers) and O^T (8 x 16) stay in
+// registers for all keys, two waves to a SIMD.  (One wave for 32 whole heads needs 144 +
+// 256 registers and spills.)  K is read from LDS 16 bytes a lane, V by
+// transposed reads of the same bytes.
+//
+// Rows of a tile come from anywhere in the cache, one kilobyte-long row a
+// load instruction (bf16), straight into LDS, while the previous tile is computed.  Rows
+// that are not selected are loaded as zeros: what the cache holds there is
+// never used.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "latent_device.h"
+#include "latent_internal.h"
+
+namespace latent {
+namespace {
+
+constexpr int kLatentSteps = kLatent / 32;   // a wave's 16 steps of the first product
+constexpr int kRopeSteps = kRope / 32;       // and 2 of the rotary part
+constexpr int kColBlocks = kLatent / 64;     // its 8 blocks of O^T
+constexpr int kRowBytes = kLatent * 2;       // a row as bf16 in LDS
+constexpr int kRopeBytes = kRope * 2;
+constexpr int kTileLatent = kTileKeys * kRowBytes;
+constexpr int kTileCodes = kTileKeys * kLatent;
+constexpr int kTileRope = kTileKeys * kRopeBytes;
+
+__device__ __attribute__((aligned(16))) const char kZeroRow[kRowBytes] = {};
+
+// One tile's rows as they are loaded.
+template <bool E4M3>
+struct Stage {
+  char latent[E4M3 ? kTileCodes : kTileLatent];
+  char rope[kTileRope];
+};
+
+// What a wave keeps of its 32 heads and its half of the values along a row of keys.
+struct HeadState {
+  bf16x8 q[kLatentSteps + kRopeSteps];
+  f32x16 o[kColBlocks];
+  float m;      // reference maximum (log2 units)
+  float l;      // this lane's part of the sum
+};
+
+// Where the keys of a token come from.
+struct TokenKeys {
+  int64_t token;
+  int64_t len;               // keys (positions, or k)
+  const int32_t* list;       // the token's slots, or its request's pages
+};
+
+template <bool PAGED>
+__device__ __forceinline__ int tile_slot(const AttendArgs& a, const TokenKeys& tk, int64_t tile, int lane) {
+  const int64_t pos = tile * kTileKeys + (lane & (kTileKeys - 1));
+  int64_t slot = -1;
+  if (pos < tk.len) {
+    if (PAGED) {
+      const int64_t col = pos >> a.log2_page;
+      if (col < a.pages_per_row) {
+        const int64_t page = tk.list[col];
+        if (page >= 0) slot = (page << a.log2_page) + (pos & (((int64_t)1 << a.log2_page) - 1));
+      }
+    } else {
+      slot = tk.list[pos];
+    }
+  }
+  return slot >= 0 && slot < a.cache.num_slots ? (int)slot : -1;
+}
+
+// Queues the loads of a tile's rows; `slots`: lane i (mod 32) holds key i's.
+template <int NW, bool E4M3>
+__device__ __forceinline__ void load_tile(const Cache& c, int slots, Stage<E4M3>& st, int lane, int wave) {
+  if (E4M3) {
+    constexpr int kEach = kTileKeys / 2 / NW;   // two rows an instruction
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int pair = wave * kEach + i;
+      const int s0 = __builtin_amdgcn_readlane(slots, 2 * pair), s1 = __builtin_amdgcn_readlane(slots, 2 * pair + 1);
+      const char* r0 = s0 >= 0 ? c.latent + (int64_t)s0 * c.latent_stride : kZeroRow;
+      const char* r1 = s1 >= 0 ? c.latent + (int64_t)s1 * c.latent_stride : kZeroRow;
+      load_to_lds((lane < 32 ? r0 : r1) + (lane & 31) * 16, st.latent + pair * 2 * kLatent);
+    }
+  } else {
+    constexpr int kEach = kTileKeys / NW;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int key = wave * kEach + i;
+      const int s = __builtin_amdgcn_readlane(slots, key);
+      const char* row = s >= 0 ? c.latent + (int64_t)s * c.latent_stride : kZeroRow;
+      load_to_lds(row + (lane ^ swizzle(key)) * 16, st.latent + key * kRowBytes);
+    }
+  }
+  constexpr int kRopeEach = NW < 4 ? 4 / NW : 1;   // eight rows an instruction
+  if (NW > 4 && wave >= 4) return;
+#pragma unroll
+  for (int i = 0; i < kRopeEach; ++i) {
+    const int group = wave * kRopeEach + i;
+    const int key = group * 8 + (lane >> 3);
+    const int s = __shfl(slots, key);
+    const char* row = s >= 0 ? c.rope + (int64_t)s * c.rope_stride : kZeroRow;
+    load_to_lds(row + ((lane ^ key) & 7) * 16, st.rope + group * 8 * kRopeBytes);
+  }
+}
+
+// E4M3 rows of a stage as bf16 rows (exact), in the layout bf16 rows are loaded in.
+template <int NW>
+__device__ __forceinline__ void widen_tile(const char* codes, char* lat, int tid) {
+#pragma unroll
+  for (int i = 0; i < kTileCodes / 16 / (64 * NW); ++i) {
+    const int at = i * 64 * NW + tid;
+    const int key = at >> 5, c = (at & 31) * 2, sw = swizzle(key);
+    const uint4 v = *reinterpret_cast<const uint4*>(codes + at * 16);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bf16x8 o[2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k], 1.0f, false);
+      const bf16x2 r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k], 1.0f, true);
+      o[k >> 1][(k & 1) * 4 + 0] = p[0];
+      o[k >> 1][(k & 1) * 4 + 1] = p[1];
+      o[k >> 1][(k & 1) * 4 + 2] = r[0];
+      o[k >> 1][(k & 1) * 4 + 3] = r[1];
+    }
+    *reinterpret_cast<bf16x8*>(lat + key * kRowBytes + (c ^ sw) * 16) = o[0];
+    *reinterpret_cast<bf16x8*>(lat + key * kRowBytes + ((c + 1) ^ sw) * 16) = o[1];
+  }
+}
+
+// A wave's part of a tile's scores: its half of the values.  scales (E4M3):
+// each key's scale.
+template <bool E4M3>
+__device__ __forceinline__ f32x16 score_tile(const HeadState& st, const char* lat, const char* rope,
+                                             const float* scales, int half, int lane) {
+  const int i = lane & 31, hb = lane >> 5;
+  f32x16 s = {};
+  {
+    const char* row = lat + i * kRowBytes + half * (kRowBytes / 2);
+    const int sw = swizzle(i);
+#pragma unroll
+    for (int k = 0; k < kLatentSteps; ++k) {
+      const bf16x8 key = *reinterpret_cast<const bf16x8*>(row + (k >> 3) * 256 + (((2 * (k & 7) + hb) ^ sw) << 4));
+      s = mfma(key, st.q[k], s);
+    }
+  }
+  if (E4M3) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[4 * g + e] *= sc[e];
+    }
+  }
+  {
+    const char* row = rope + i * kRopeBytes;
+#pragma unroll
+    for (int k = 0; k < kRopeSteps; ++k) {
+      const bf16x8 key =
+          *reinterpret_cast<const bf16x8*>(row + (((2 * (half * kRopeSteps + k) + hb) ^ i) & 7) * 16);
+      s = mfma(key, st.q[kLatentSteps + k], s);
+    }
+  }
+  return s;
+}
+
+// The softmax step and the second product of a tile whose scores are s.
+// mask: the tile's selected keys.
+template <bool E4M3>
+__device__ __forceinline__ void weigh_tile(HeadState& st, f32x16 s, const char* lat, const float* scales,
+                                           uint32_t mask, float scale_log2, int half, int lane) {
+  const int hb = lane >> 5;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s[r] *= scale_log2;
+  if (mask != 0xFFFFFFFFu) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (!((mask >> acc_row(r, hb)) & 1)) s[r] = -INFINITY;
+  }
+  float top = s[0];
+#pragma unroll
+  for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+  top = fmaxf(top, other_half(top, lane));
+  if (__any(top > st.m + kLazy)) {
+    const float m = fmaxf(st.m, top);
+    const float f = __builtin_amdgcn_exp2f(st.m - m);
+    st.m = m;
+    st.l *= f;
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) st.o[cb][r] *= f;
+  }
+  // Weights in bf16 (the matrix cores' type): an unbiased half step of 2^-9 on
+  // each, as large as the rounding of the result itself.  The sum keeps them in fp32.
+  bf16x8 p[2];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    f32x4 sc = {1.f, 1.f, 1.f, 1.f};
+    if (E4M3) sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w = __builtin_amdgcn_exp2f(s[4 * g + e] - st.m);
+      st.l += w;
+      p[g >> 1][(g & 1) * 4 + e] = (__bf16)(E4M3 ? w * sc[e] : w);
+    }
+  }
+  const int j = lane & 15, quarter = (lane >> 4) & 1;
+  lat += half * (kRowBytes / 2);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb) {
+      const int chunk = (cb & 3) * 4 + 2 * quarter + ((j & 3) >> 1);
+      bf16x4 v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int key = 16 * k + 8 * e + 4 * hb + (j >> 2);
+        v[e] = read_tr(lat + key * kRowBytes + (cb >> 2) * 256 + ((chunk ^ swizzle(key)) << 4) + (j & 1) * 8);
+      }
+      st.o[cb] = mfma(join8(v[0], v[1]), p[k], st.o[cb]);
+    }
+  }
+}
+
+// Last of the n ascending starts at or below v, 64 at a time; wave-uniform.
+__device__ __forceinline__ int64_t count_starts(const int32_t* starts, int64_t n, int64_t v, int lane) {
+  int64_t c = 0;
+  for (int64_t base = 1; base <= n; base += 64) {
+    const int64_t at = base + lane;
+    const int got = __popcll(__ballot(at <= n && (int64_t)starts[at <= n ? at : n] <= v));
+    c += got;
+    if (got < 64) break;
+  }
+  return c;
+}
+
+// Keys that token t, of request b, attends; those past the page table's row
+// have no page.
+__device__ __forceinline__ int64_t token_len(const AttendArgs& a, int64_t t, int64_t b) {
+  const int64_t len = (int64_t)a.seq_lens[b] - ((int64_t)a.q_starts[b + 1] - t) + 1;
+  const int64_t most = a.pages_per_row << a.log2_page;
+  return len < 0 ? 0 : (len < most ? len : most);
+}
+
+// A split launch's plan of whole sequences: the tiles before each token, and its request.
+struct SplitPlan {
+  int32_t start[kSplitTokens + 1];
+  uint16_t request[kSplitTokens];
+};
+
+// A token's tiles; one even when it has no key, so that somebody writes its row.
+__device__ __forceinline__ int64_t token_tiles(int64_t len) {
+  const int64_t n = (len + kTileKeys - 1) / kTileKeys;
+  return n > 0 ? n : 1;
+}
+
+template <int NW>
+__device__ void plan_split(const AttendArgs& a, SplitPlan& plan, int tid) {
+  const int T = a.num_tokens;
+  for (int t = tid; t <= T; t += 64 * NW) plan.start[t] = 0;
+  lds_barrier();
+  // request index + 1 at each request's first token, then carried along
+  for (int b = tid; b < a.num_requests; b += 64 * NW) {
+    const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1];
+    if (q1 > q0 && q0 >= 0 && q0 < T) plan.start[q0] = b + 1;
+  }
+  lds_barrier();
+  const int end = a.q_starts[a.num_requests];
+  if (tid < 64) {
+    int carry = 0;
+    for (int base = 0; base < T; base += 64) {
+      const int t = base + tid;
+      int v = t < T ? plan.start[t] : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (tid >= d) v = v > o ? v : o;
+      }
+      v = v > carry ? v : carry;
+      carry = __shfl(v, 63);
+      if (t < T) plan.request[t] = (uint16_t)(v > 0 ? v - 1 : 0);
+    }
+    int sum = 0;
+    for (int base = 0; base < T; base += 64) {
+      const int t = base + tid;
+      int n = 0;
+      if (t < T && t < end) n = (int)token_tiles(token_len(a, t, plan.request[t]));
+      int v = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (tid >= d) v += o;
+      }
+      if (t < T) plan.start[t] = sum + v - n;
+      sum += __shfl(v, 63);
+    }
+    if (tid == 0) plan.start[T] = sum;
+  }
+  lds_barrier();
+}
+
+template <int PAIRS, bool E4M3, bool PAGED>
+__global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
+  constexpr int NW = 2 * PAIRS;
+  __shared__ __attribute__((aligned(16))) Stage<E4M3> stage0, stage1;
+  __shared__ __attribute__((aligned(16))) char wide[E4M3 ? kTileLatent : 16];
+  __shared__ __attribute__((aligned(16))) float scales[NW][kTileKeys];
+  __shared__ __attribute__((aligned(16))) float swap[NW][16 * 64];
+  __shared__ SplitPlan plan;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pair = wave >> 1, half = wave & 1;
+  const int head0 = (blockIdx.y * PAIRS + pair) * 32;
+  const int head = head0 + (lane & 31), hb = lane >> 5;
+  const bool live_wave = head0 < a.num_heads;
+  const bool split = a.wgs > 0;
+
+  // this workgroup's tiles [lo, hi) of all tokens' tiles, beginning in token t
+  int64_t lo, hi, t, total = 0;
+  int wgs = 1;
+  const int64_t k_tiles = token_tiles(a.k);
+  if (split) {
+    if (PAGED) {
+      plan_split<NW>(a, plan, tid);
+      total = plan.start[a.num_tokens];
+    } else {
+      total = a.num_tokens * k_tiles;
+    }
+    wgs = (int)(a.wgs < total ? a.wgs : total);
+    if ((int)blockIdx.x >= wgs) return;
+    lo = total * blockIdx.x / wgs;
+    hi = total * (blockIdx.x + 1) / wgs;
+    if (PAGED) {
+      int l = 0, h = a.num_tokens;
+      while (h - l > 1) {
+        const int mid = (l + h) >> 1;
+        if (plan.start[mid] <= lo) l = mid; else h = mid;
+      }
+      t = __builtin_amdgcn_readfirstlane(l);
+    } else {
+      t = lo / k_tiles;
+    }
+  } else {
+    // neighbouring tokens select neighbouring rows: each XCD (workgroups are
+    // dealt to the 8 of them in turn) takes a contiguous share of the tokens
+    const int64_t per = ((int64_t)a.num_tokens + 7) / 8;
+    t = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || t >= a.num_tokens) return;
+    if (PAGED && t >= (int64_t)a.q_starts[a.num_requests]) return;
+    lo = 0;
+    hi = INT64_MAX;
+  }
+
+  while (lo < hi) {
+    // the part [first, last) of token t's n tiles
+    TokenKeys tk;
+    tk.token = t;
+    int64_t first = lo, last = hi, n;
+    if (PAGED) {
+      const int64_t b = split ? (int64_t)__builtin_amdgcn_readfirstlane((int)plan.request[t])
+                              : count_starts(a.q_starts, a.num_requests, t, lane);
+      tk.len = token_len(a, t, b);
+      tk.list = a.page_table + b * a.pages_per_row;
+    } else {
+      tk.len = a.k;
+      tk.list = a.indices + t * a.k;
+    }
+    n = token_tiles(tk.len);
+    int64_t start = 0;
+    if (split) {
+      start = PAGED ? (int64_t)__builtin_amdgcn_readfirstlane(plan.start[t]) : t * k_tiles;
+      first = lo - start;
+      last = hi - start;
+    }
+    if (last > n) last = n;
+    const bool whole = first == 0 && last == n;
+
+    HeadState st;
+    st.m = kNoMax;
+    st.l = 0.f;
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x16{};
+    {
+      const uint16_t* q = a.q + t * a.q_token_stride + (int64_t)head * a.q_head_stride + hb * 8;
+#pragma unroll
+      for (int k = 0; k < kLatentSteps + kRopeSteps; ++k) {
+        const int at = k < kLatentSteps ? (half * kLatentSteps + k) * 16
+                                        : kLatent + (half * kRopeSteps + k - kLatentSteps) * 16;
+        st.q[k] = bf16x8{};
+        if (head < a.num_heads) st.q[k] = *reinterpret_cast<const bf16x8*>(q + at);
+      }
+    }
+
+    int slots = tile_slot<PAGED>(a, tk, first, lane);           // of the tile being loaded
+    lds_barrier();                                              // the last part's reads are done
+    load_tile<NW, E4M3>(a.cache, slots, stage0, lane, wave);
+    float scale = E4M3 && slots >= 0 ? a.cache.scale[slots] : 0.f;
+    int next = first + 1 < last ? tile_slot<PAGED>(a, tk, first + 1, lane) : -1;
+
+    auto step = [&](int64_t tile, Stage<E4M3>& cur, Stage<E4M3>& nxt) {
+      const uint32_t mask = (uint32_t)__ballot(slots >= 0);
+      if (E4M3 && lane < kTileKeys) scales[wave][lane] = scale;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      lds_barrier();            // every wave's rows are there, and nobody reads the other stage any more
+      if (tile + 1 < last) {
+        slots = next;
+        load_tile<NW, E4M3>(a.cache, slots, nxt, lane, wave);
+        scale = E4M3 && slots >= 0 ? a.cache.scale[slots] : 0.f;
+        next = tile + 2 < last ? tile_slot<PAGED>(a, tk, tile + 2, lane) : -1;
+      }
+      if (mask == 0) return;
+      if (E4M3) {
+        widen_tile<NW>(cur.latent, wide, tid);
+        lds_barrier();
+      }
+      const char* lat = E4M3 ? wide : cur.latent;
+      f32x16 s = {};
+      if (live_wave) {
+        s = score_tile<E4M3>(st, lat, cur.rope, scales[wave], half, lane);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4*>(&swap[wave][g * 256 + lane * 4]) = f32x4{s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]};
+      }
+      lds_barrier();
+      if (live_wave) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 o = *reinterpret_cast<const f32x4*>(&swap[wave ^ 1][g * 256 + lane * 4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[4 * g + e] += o[e];
+        }
+        weigh_tile<E4M3>(st, s, lat, scales[wave], mask, a.scale_log2, half, lane);
+      }
+    };
+    for (int64_t tile = first; tile < last; tile += 2) {
+      step(tile, stage0, stage1);
+      if (tile + 1 < last) step(tile + 1, stage1, stage0);
+    }
+
+    // this lane's head: its sum is spread over the two half-waves
+    const float l = st.l + other_half(st.l, lane);
+    if (whole) {
+      if (head < a.num_heads) {
+        const float inv = l > 0.f ? 1.0f / l : 0.f;
+        const int64_t row = t * a.num_heads + head;
+        uint16_t* out = a.out + row * kLatent + half * (kLatent / 2) + 4 * hb;
+#pragma unroll
+        for (int cb = 0; cb < kColBlocks; ++cb)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            bf16x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (__bf16)(st.o[cb][4 * g + e] * inv);
+            *reinterpret_cast<bf16x4*>(out + cb * 32 + 8 * g) = v;
+          }
+        if (a.lse && hb == 0 && half == 0) a.lse[row] = l > 0.f ? (st.m + __log2f(l)) * kLn2 : -INFINITY;
+      }
+      if (split && tid == 0 && blockIdx.y == 0) {
+        a.part_rec[2 * t] = 0;
+        a.part_rec[2 * t + 1] = 1;
+      }
+    } else {
+      // a part that begins its token is this workgroup's last, any other its first
+      const int64_t slot = first == 0 ? a.wgs + blockIdx.x : blockIdx.x;
+      const int64_t at = ((int64_t)blockIdx.y * 2 * a.wgs + slot) * NW + wave;
+      if (live_wave) {
+        float* o = a.part_out + at * (16 * kLatent) + lane * 4;
+#pragma unroll
+        for (int cb = 0; cb < kColBlocks; ++cb)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = st.o[cb][4 * g + e];
+            *reinterpret_cast<f32x4*>(o + (cb * 4 + g) * 256) = v;
+          }
+        if (hb == 0) a.part_ml[at * 32 + lane] = make_float2(st.m, l);   // the same in both waves of a pair
+      }
+      if (first == 0 && tid == 0 && blockIdx.y == 0) {
+        // the last of its tiles is held by the last workgroup g with total g / wgs <= that tile
+        const int64_t g1 = ((start + n) * wgs - 1) / total;
+        a.part_rec[2 * t] = (int32_t)blockIdx.x;
+        a.part_rec[2 * t + 1] = (int32_t)(g1 - blockIdx.x + 1);
+      }
+    }
+    if (!split) return;
+    lo = start + last;
+    ++t;
+  }
+}
+
+// Joins the parts of a token: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.
+// A workgroup takes 32 heads and one block of 32 latent values, a wave 8 of
+// these: elements stay in the accumulators' order, so reads are contiguous.
+template <int PAIRS>
+__global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
+  constexpr int NW = 2 * PAIRS;
+  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  const int heads = blockIdx.y, half = blockIdx.z / kColBlocks, cb = blockIdx.z % kColBlocks;
+  if (!a.indices && t >= (int64_t)a.q_starts[a.num_requests]) return;
+  const int g0 = a.part_rec[2 * t], parts = a.part_rec[2 * t + 1];
+  if (parts <= 1) return;
+  const int64_t base = (int64_t)(heads / PAIRS) * 2 * a.wgs;
+  const int wave = 2 * (heads % PAIRS) + half;
+  const int i = lane & 31, hb = lane >> 5;
+  auto place = [&](int p) { return (base + (p == 0 ? a.wgs + g0 : g0 + p)) * NW + wave; };
+  float m = kNoMax;
+  for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[place(p) * 32 + i].x);
+  float l = 0.f;
+  f32x4 o = {};
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = a.part_ml[place(p) * 32 + i];
+    const f32x4 v = *reinterpret_cast<const f32x4*>(a.part_out + place(p) * (16 * kLatent) + (cb * 4 + g) * 256 + lane * 4);
+    const float f = __builtin_amdgcn_exp2f(ml.x - m);
+    l = fmaf(f, ml.y, l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = fmaf(f, v[e], o[e]);
+  }
+  const int head = heads * 32 + i;
+  if (head >= a.num_heads) return;
+  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const int64_t row = t * a.num_heads + head;
+  bf16x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (__bf16)(o[e] * inv);
+  *reinterpret_cast<bf16x4*>(a.out + row * kLatent + half * (kLatent / 2) + cb * 32 + 8 * g + 4 * hb) = v;
+  if (a.lse && blockIdx.z == 0 && g == 0 && hb == 0) a.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+}
+
+int head_blocks(int num_heads, int pairs) { return (num_heads + 32 * pairs - 1) / (32 * pairs); }
+
+template <int PAIRS, bool E4M3>
+hipError_t launch(const AttendArgs& a, hipStream_t stream) {
+  const unsigned x = a.wgs > 0 ? (unsigned)a.wgs : (unsigned)(((int64_t)a.num_tokens + 7) / 8 * 8);
+  const dim3 grid(x, (unsigned)head_blocks(a.num_heads, PAIRS)), block(128 * PAIRS);
+  if (a.indices)
+    hipLaunchKernelGGL((attend_kernel<PAIRS, E4M3, false>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((attend_kernel<PAIRS, E4M3, true>), grid, block, 0, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.wgs == 0) return e;
+  hipLaunchKernelGGL(join_kernel<PAIRS>, dim3((unsigned)a.num_tokens, (unsigned)((a.num_heads + 31) / 32), 2 * kColBlocks),
+                     dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int attend_pairs(int num_heads) { return num_heads <= 32 ? 1 : (num_heads <= 64 ? 2 : 4); }
+
+SplitLayout split_layout(int num_tokens, int num_heads, int wgs) {
+  const int pairs = attend_pairs(num_heads);
+  const size_t parts = (size_t)2 * wgs * head_blocks(num_heads, pairs) * 2 * pairs;   // of one wave
+  SplitLayout s;
+  s.out_bytes = parts * 16 * kLatent * sizeof(float);
+  s.ml_bytes = parts * 32 * sizeof(float2);
+  s.rec_bytes = ((size_t)num_tokens * 2 * sizeof(int32_t) + 15) / 16 * 16;
+  return s;
+}
+
+hipError_t launch_attend(const AttendArgs& a, bool e4m3, hipStream_t stream) {
+  switch (attend_pairs(a.num_heads)) {
+    case 1: return e4m3 ? launch<1, true>(a, stream) : launch<1, false>(a, stream);
+    case 2: return e4m3 ? launch<2, true>(a, stream) : launch<2, false>(a, stream);
+    default: return e4m3 ? launch<4, true>(a, stream) : launch<4, false>(a, stream);
+  }
+}
+
+}  // namespace latent

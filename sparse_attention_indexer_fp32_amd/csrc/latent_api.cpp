@@ -1,0 +1,397 @@
+// C-ABI layer of the paged latent cache and of latent attention: argument and
+// device checks, launch shapes.  Nothing is allocated or kept here but the
+// number of CUs of each device seen.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdio>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <string>
+
+#include "latent_attention.h"
+#include "latent_internal.h"
+#include "topk_internal.h"
+
+namespace {
+
+std::map<int, int> g_cus;   // device -> CUs, 0 when it is not gfx950; under the library's lock
+
+topk_status_t fail(topk_status_t st, const char* msg) {
+  topk::set_last_error(msg);
+  return st;
+}
+
+topk_status_t invalid(const char* msg) { return fail(TOPK_ERROR_INVALID_VALUE, msg); }
+
+topk_status_t launched(hipError_t e, const char* what) {
+  if (e == hipSuccess) {
+    topk::set_last_launch(what);
+    return TOPK_SUCCESS;
+  }
+  char buf[256];
+  std::snprintf(buf, sizeof(buf), "%s launch: %s", what, hipGetErrorString(e));
+  return fail(TOPK_ERROR_LAUNCH, buf);
+}
+
+// CUs of the current device; TOPK_ERROR_UNSUPPORTED when it is not gfx950.
+topk_status_t device_cus(int* cus) {
+  std::lock_guard<std::mutex> lock(topk::lib_mutex());
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return fail(TOPK_ERROR_LAUNCH, "hipGetDevice failed");
+  auto it = g_cus.find(dev);
+  if (it == g_cus.end()) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
+      return fail(TOPK_ERROR_LAUNCH, "hipGetDeviceProperties failed");
+    const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+    it = g_cus.emplace(dev, ok ? prop.multiProcessorCount : 0).first;
+  }
+  if (it->second == 0) return fail(TOPK_ERROR_UNSUPPORTED, "device is not gfx950");
+  *cus = it->second;
+  return TOPK_SUCCESS;
+}
+
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int log2_of(int32_t page_size) {
+  if (page_size < 1 || (page_size & (page_size - 1)) != 0) return -1;
+  return __builtin_ctz((unsigned)page_size);
+}
+
+// The cache's arrays; strides in elements in, bytes out.
+topk_status_t check_cache(const void* latent, int64_t latent_stride, const uint16_t* rope, int64_t rope_stride,
+                          const float* scale, int32_t cache_type, int64_t num_slots, latent::Cache* c) {
+  if (cache_type != LATENT_CACHE_BF16 && cache_type != LATENT_CACHE_E4M3)
+    return invalid("cache_type must be LATENT_CACHE_BF16 or LATENT_CACHE_E4M3");
+  const bool e4m3 = cache_type == LATENT_CACHE_E4M3;
+  if (num_slots < 0 || num_slots > (int64_t)INT32_MAX) return invalid("num_slots must be in [0, 2^31)");
+  if (num_slots > 0 && (!latent || !rope)) return invalid("latent and rope must be non-null when num_slots > 0");
+  if (e4m3 && num_slots > 0 && !scale) return invalid("an E4M3 cache needs its scales");
+  if (!e4m3 && scale) return invalid("a bf16 cache has no scales");
+  const int64_t lb = latent_stride * (e4m3 ? 1 : 2), rb = rope_stride * 2;
+  if (latent_stride < LATENT_DIM || rope_stride < LATENT_ROPE_DIM)
+    return invalid("cache rows overlap: latent_stride >= 512 and rope_stride >= 64 are needed");
+  if (latent_stride > (int64_t)1 << 31 || rope_stride > (int64_t)1 << 31) return invalid("cache row stride too large");
+  if (!aligned(latent) || !aligned(rope) || lb % 16 != 0 || rb % 16 != 0)
+    return invalid("cache rows must start on 16-byte boundaries");
+  c->latent = static_cast<const char*>(latent);
+  c->rope = reinterpret_cast<const char*>(rope);
+  c->scale = scale;
+  c->latent_stride = lb;
+  c->rope_stride = rb;
+  c->num_slots = num_slots;
+  return TOPK_SUCCESS;
+}
+
+// Workgroups that share the tiles of a launch of absorbed attention, or 0 for one
+// workgroup per token.  Two workgroups of up to 64 heads fit a CU, one of 128.
+int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, int32_t num_requests) {
+  const int pairs = latent::attend_pairs(num_heads);
+  const int64_t blocks = (num_heads + 32 * pairs - 1) / (32 * pairs);
+  const int64_t resident = (int64_t)cus * (pairs == 4 ? 1 : 2);
+  if (num_tokens > latent::kSplitTokens || num_requests > 65535 || num_tokens * blocks >= 4 * resident) return 0;
+  int64_t wgs = resident / blocks;
+  const int64_t tiles = num_tokens * ((keys + latent::kTileKeys - 1) / latent::kTileKeys + 1);
+  if (tiles > (int64_t)INT32_MAX) return 0;   // the plan counts tiles in 32 bits
+  if (wgs > tiles) wgs = tiles;
+  return wgs < 1 ? 1 : (int)wgs;
+}
+
+topk_status_t check_queries(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const uint16_t* out,
+                            int32_t num_tokens, int32_t num_heads, int width) {
+  if (num_tokens < 0 || num_heads < 0) return invalid("num_tokens and num_heads must be >= 0");
+  if (num_tokens == 0 || num_heads == 0) return TOPK_SUCCESS;
+  if (!q || !out) return invalid("q and out must be non-null");
+  if (q_token_stride < 0 || q_head_stride < 0 || (num_heads > 1 && q_head_stride < width))
+    return invalid("q's heads overlap, or a stride is negative");
+  if (!aligned(q) || !aligned(out) || q_token_stride % 8 != 0 || q_head_stride % 8 != 0)
+    return invalid("q's rows and out must start on 16-byte boundaries");
+  return TOPK_SUCCESS;
+}
+
+// The launch of an absorbed call whose arguments hold; a's workspace from the caller's.
+topk_status_t attend(latent::AttendArgs& a, int64_t keys, bool e4m3, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream) {
+  int cus = 0;
+  const topk_status_t st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  a.wgs = split_wgs(cus, a.num_tokens, a.num_heads, keys, a.num_requests);
+  if (a.wgs > 0) {
+    const latent::SplitLayout s = latent::split_layout(a.num_tokens, a.num_heads, a.wgs);
+    if (!workspace || workspace_bytes < s.total()) return invalid("the workspace is smaller than latent_attention_workspace says");
+    if (!aligned(workspace)) return invalid("the workspace must start on a 16-byte boundary");
+    char* p = static_cast<char*>(workspace);
+    a.part_out = reinterpret_cast<float*>(p);
+    a.part_ml = reinterpret_cast<float2*>(p + s.out_bytes);
+    a.part_rec = reinterpret_cast<int32_t*>(p + s.out_bytes + s.ml_bytes);
+  }
+  char buf[160];
+  std::snprintf(buf, sizeof(buf), "latent-attention %s %s pairs=%d wgs=%d", a.indices ? "selected" : "paged",
+                e4m3 ? "e4m3" : "bf16", latent::attend_pairs(a.num_heads), a.wgs);
+  return launched(latent::launch_attend(a, e4m3, stream), buf);
+}
+
+}  // namespace
+
+extern "C" {
+
+topk_status_t paged_append_plan(const int32_t* kv_lens, const int32_t* new_lens, int32_t* page_table,
+                                const int32_t* free_pages, const int32_t* free_used, int32_t page_size,
+                                int32_t* seq_lens, int32_t* q_starts, int32_t* slot_map, int32_t* positions,
+                                int32_t* free_used_out, hipStream_t stream, int32_t num_requests,
+                                int64_t pages_per_row, int64_t num_free, int64_t num_tokens) {
+  topk::set_last_error("");
+  const int log2_page = log2_of(page_size);
+  if (log2_page < 0) return invalid("page_size must be a power of two");
+  if (num_requests < 0 || pages_per_row < 0 || num_free < 0 || num_tokens < 0)
+    return invalid("num_requests, pages_per_row, num_free and num_tokens must be >= 0");
+  if (num_free > (int64_t)INT32_MAX || num_tokens > (int64_t)INT32_MAX || pages_per_row > (int64_t)INT32_MAX)
+    return invalid("num_free, num_tokens and pages_per_row must fit in int32");
+  if (!q_starts || !free_used_out) return invalid("q_starts and free_used_out must be non-null");
+  if (free_used == free_used_out) return invalid("free_used_out must not be free_used");
+  if (num_requests > 0 && (!kv_lens || !new_lens || !seq_lens)) return invalid("kv_lens, new_lens and seq_lens must be non-null");
+  if (num_requests > 0 && pages_per_row > 0 && !page_table) return invalid("page_table must be non-null");
+  if (num_free > 0 && !free_pages) return invalid("free_pages must be non-null");
+  if (num_tokens > 0 && (!slot_map || !positions)) return invalid("slot_map and positions must be non-null");
+  int cus = 0;
+  const topk_status_t st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  latent::PlanArgs a{};
+  a.kv_lens = kv_lens;
+  a.new_lens = new_lens;
+  a.page_table = page_table;
+  a.free_pages = free_pages;
+  a.free_used = free_used;
+  a.seq_lens = seq_lens;
+  a.q_starts = q_starts;
+  a.slot_map = slot_map;
+  a.positions = positions;
+  a.free_used_out = free_used_out;
+  a.pages_per_row = pages_per_row;
+  a.num_free = num_free;
+  a.num_tokens = num_tokens;
+  a.num_requests = num_requests;
+  a.log2_page = log2_page;
+  return launched(latent::launch_append_plan(a, stream), "paged-append-plan");
+}
+
+topk_status_t latent_cache_store(const uint16_t* kv, int64_t kv_stride, const uint16_t* norm_weight, float eps,
+                                 const int32_t* positions, const float* cos_sin, int64_t max_positions,
+                                 int32_t interleaved, const int32_t* slot_map, void* latent, int64_t latent_stride,
+                                 uint16_t* rope, int64_t rope_stride, float* scale, int32_t cache_type,
+                                 hipStream_t stream, int64_t num_tokens, int64_t num_slots) {
+  topk::set_last_error("");
+  latent::Cache c{};
+  topk_status_t st = check_cache(latent, latent_stride, rope, rope_stride, scale, cache_type, num_slots, &c);
+  if (st != TOPK_SUCCESS) return st;
+  if (num_tokens < 0 || num_tokens > (int64_t)INT32_MAX) return invalid("num_tokens must be in [0, 2^31)");
+  if (num_tokens == 0) return TOPK_SUCCESS;
+  if (!kv || !slot_map) return invalid("kv and slot_map must be non-null");
+  if (kv_stride < LATENT_DIM + LATENT_ROPE_DIM || kv_stride % 8 != 0 || !aligned(kv))
+    return invalid("kv's rows must not overlap and must start on 16-byte boundaries");
+  if (norm_weight && !aligned(norm_weight)) return invalid("norm_weight must start on a 16-byte boundary");
+  if (cos_sin && (!positions || max_positions < 0)) return invalid("cos_sin needs positions and max_positions >= 0");
+  int cus = 0;
+  st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  latent::StoreArgs a{};
+  a.kv = kv;
+  a.kv_stride = kv_stride;
+  a.norm_weight = norm_weight;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.max_positions = max_positions;
+  a.slot_map = slot_map;
+  a.latent = static_cast<char*>(latent);
+  a.rope = reinterpret_cast<char*>(rope);
+  a.scale = scale;
+  a.latent_stride = c.latent_stride;
+  a.rope_stride = c.rope_stride;
+  a.num_tokens = num_tokens;
+  a.num_slots = num_slots;
+  a.eps = eps;
+  a.interleaved = interleaved;
+  return launched(latent::launch_cache_store(a, cache_type == LATENT_CACHE_E4M3, stream), "latent-cache-store");
+}
+
+topk_status_t latent_cache_load(const int32_t* slots, const void* latent, int64_t latent_stride, const uint16_t* rope,
+                                int64_t rope_stride, const float* scale, int32_t cache_type, uint16_t* out_latent,
+                                uint16_t* out_rope, hipStream_t stream, int64_t num_rows, int64_t num_slots) {
+  topk::set_last_error("");
+  latent::LoadArgs a{};
+  topk_status_t st = check_cache(latent, latent_stride, rope, rope_stride, scale, cache_type, num_slots, &a.cache);
+  if (st != TOPK_SUCCESS) return st;
+  if (num_rows < 0 || num_rows > (int64_t)INT32_MAX) return invalid("num_rows must be in [0, 2^31)");
+  if (num_rows == 0) return TOPK_SUCCESS;
+  if (!slots || !out_latent || !out_rope) return invalid("slots, out_latent and out_rope must be non-null");
+  if (!aligned(out_latent) || !aligned(out_rope)) return invalid("out_latent and out_rope must start on 16-byte boundaries");
+  int cus = 0;
+  st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  a.slots = slots;
+  a.out_latent = out_latent;
+  a.out_rope = out_rope;
+  a.num_rows = num_rows;
+  return launched(latent::launch_cache_load(a, cache_type == LATENT_CACHE_E4M3, stream), "latent-cache-load");
+}
+
+topk_status_t latent_cache_load_paged(const int32_t* page_table, const int32_t* kv_starts, int32_t page_size,
+                                      const void* latent, int64_t latent_stride, const uint16_t* rope,
+                                      int64_t rope_stride, const float* scale, int32_t cache_type,
+                                      uint16_t* out_latent, uint16_t* out_rope, hipStream_t stream,
+                                      int32_t num_requests, int64_t pages_per_row, int64_t num_rows,
+                                      int64_t num_slots) {
+  topk::set_last_error("");
+  latent::LoadArgs a{};
+  topk_status_t st = check_cache(latent, latent_stride, rope, rope_stride, scale, cache_type, num_slots, &a.cache);
+  if (st != TOPK_SUCCESS) return st;
+  a.log2_page = log2_of(page_size);
+  if (a.log2_page < 0) return invalid("page_size must be a power of two");
+  if (num_rows < 0 || num_rows > (int64_t)INT32_MAX) return invalid("num_rows must be in [0, 2^31)");
+  if (num_requests < 0 || pages_per_row < 0) return invalid("num_requests and pages_per_row must be >= 0");
+  if (num_rows == 0 || num_requests == 0) return TOPK_SUCCESS;
+  if (!kv_starts || !out_latent || !out_rope) return invalid("kv_starts, out_latent and out_rope must be non-null");
+  if (pages_per_row > 0 && !page_table) return invalid("page_table must be non-null");
+  if (!aligned(out_latent) || !aligned(out_rope)) return invalid("out_latent and out_rope must start on 16-byte boundaries");
+  int cus = 0;
+  st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  a.page_table = page_table;
+  a.kv_starts = kv_starts;
+  a.pages_per_row = pages_per_row;
+  a.out_latent = out_latent;
+  a.out_rope = out_rope;
+  a.num_rows = num_rows;
+  a.num_requests = num_requests;
+  return launched(latent::launch_cache_load(a, cache_type == LATENT_CACHE_E4M3, stream), "latent-cache-load paged");
+}
+
+topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, int64_t keys, size_t* bytes) {
+  topk::set_last_error("");
+  if (!bytes) return invalid("bytes must be non-null");
+  if (num_tokens < 0 || num_heads < 0 || keys < 0) return invalid("num_tokens, num_heads and keys must be >= 0");
+  *bytes = 0;
+  if (num_tokens == 0 || num_heads == 0) return TOPK_SUCCESS;
+  int cus = 0;
+  const topk_status_t st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  const int wgs = split_wgs(cus, num_tokens, num_heads, keys, 0);
+  if (wgs > 0) *bytes = latent::split_layout(num_tokens, num_heads, wgs).total();
+  return TOPK_SUCCESS;
+}
+
+topk_status_t latent_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const void* latent,
+                               int64_t latent_stride, const uint16_t* rope, int64_t rope_stride, const float* scale,
+                               int32_t cache_type, const int32_t* indices, float softmax_scale, uint16_t* out,
+                               float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                               int32_t num_tokens, int32_t num_heads, int64_t k, int64_t num_slots) {
+  topk::set_last_error("");
+  latent::AttendArgs a{};
+  topk_status_t st = check_cache(latent, latent_stride, rope, rope_stride, scale, cache_type, num_slots, &a.cache);
+  if (st != TOPK_SUCCESS) return st;
+  st = check_queries(q, q_token_stride, q_head_stride, out, num_tokens, num_heads, LATENT_DIM + LATENT_ROPE_DIM);
+  if (st != TOPK_SUCCESS) return st;
+  if (k < 0 || k > (int64_t)INT32_MAX) return invalid("k must be in [0, 2^31)");
+  if (num_tokens == 0 || num_heads == 0) return TOPK_SUCCESS;
+  if (k > 0 && !indices) return invalid("indices must be non-null");
+  a.q = q;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  // with k = 0 nothing is read through it, but it tells the two forms apart
+  a.indices = indices ? indices : reinterpret_cast<const int32_t*>(q);
+  a.k = k;
+  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  a.out = out;
+  a.lse = lse;
+  a.num_tokens = num_tokens;
+  a.num_heads = num_heads;
+  return attend(a, k, cache_type == LATENT_CACHE_E4M3, workspace, workspace_bytes, stream);
+}
+
+topk_status_t latent_attention_paged(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                     const void* latent, int64_t latent_stride, const uint16_t* rope,
+                                     int64_t rope_stride, const float* scale, int32_t cache_type,
+                                     const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_starts,
+                                     int32_t page_size, float softmax_scale, uint16_t* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, hipStream_t stream, int32_t num_tokens,
+                                     int32_t num_heads, int32_t num_requests, int64_t pages_per_row,
+                                     int64_t num_slots) {
+  topk::set_last_error("");
+  latent::AttendArgs a{};
+  topk_status_t st = check_cache(latent, latent_stride, rope, rope_stride, scale, cache_type, num_slots, &a.cache);
+  if (st != TOPK_SUCCESS) return st;
+  st = check_queries(q, q_token_stride, q_head_stride, out, num_tokens, num_heads, LATENT_DIM + LATENT_ROPE_DIM);
+  if (st != TOPK_SUCCESS) return st;
+  a.log2_page = log2_of(page_size);
+  if (a.log2_page < 0) return invalid("page_size must be a power of two");
+  if (num_requests < 0 || pages_per_row < 0 || pages_per_row > (int64_t)INT32_MAX)
+    return invalid("num_requests must be >= 0 and pages_per_row in [0, 2^31)");
+  if (num_tokens == 0 || num_heads == 0 || num_requests == 0) return TOPK_SUCCESS;
+  if (!seq_lens || !q_starts || (pages_per_row > 0 && !page_table))
+    return invalid("page_table, seq_lens and q_starts must be non-null");
+  a.q = q;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.q_starts = q_starts;
+  a.pages_per_row = pages_per_row;
+  a.num_requests = num_requests;
+  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  a.out = out;
+  a.lse = lse;
+  a.num_tokens = num_tokens;
+  a.num_heads = num_heads;
+  return attend(a, pages_per_row * (int64_t)page_size, cache_type == LATENT_CACHE_E4M3, workspace, workspace_bytes,
+                stream);
+}
+
+topk_status_t latent_attention_expanded(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                        const uint16_t* kv_up, int64_t kv_token_stride, int64_t kv_head_stride,
+                                        const uint16_t* rope, int64_t rope_stride, const int32_t* q_starts,
+                                        const int32_t* kv_starts, float softmax_scale, int32_t causal, uint16_t* out,
+                                        float* lse, hipStream_t stream, int32_t num_tokens, int64_t num_kv,
+                                        int32_t num_heads, int32_t num_requests) {
+  topk::set_last_error("");
+  topk_status_t st =
+      check_queries(q, q_token_stride, q_head_stride, out, num_tokens, num_heads, LATENT_HEAD_DIM + LATENT_ROPE_DIM);
+  if (st != TOPK_SUCCESS) return st;
+  if (num_kv < 0 || num_kv > (int64_t)INT32_MAX) return invalid("num_kv must be in [0, 2^31)");
+  if (num_requests < 0) return invalid("num_requests must be >= 0");
+  if (num_tokens == 0 || num_heads == 0 || num_requests == 0) return TOPK_SUCCESS;
+  if (!q_starts || !kv_starts) return invalid("q_starts and kv_starts must be non-null");
+  if (num_kv > 0 && (!kv_up || !rope)) return invalid("kv_up and rope must be non-null when num_kv > 0");
+  if (num_heads > 65535) return invalid("num_heads must be at most 65535");
+  if (kv_token_stride < 0 || kv_head_stride < 0 || (num_heads > 1 && kv_head_stride < 2 * LATENT_HEAD_DIM) ||
+      rope_stride < LATENT_ROPE_DIM)
+    return invalid("kv_up's heads or rope's rows overlap, or a stride is negative");
+  if (!aligned(kv_up) || !aligned(rope) || kv_token_stride % 8 != 0 || kv_head_stride % 8 != 0 || rope_stride % 8 != 0)
+    return invalid("kv_up's and rope's rows must start on 16-byte boundaries");
+  int cus = 0;
+  st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  latent::PrefillArgs a{};
+  a.q = q;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.kv = kv_up;
+  a.kv_token_stride = kv_token_stride;
+  a.kv_head_stride = kv_head_stride;
+  a.rope = rope;
+  a.rope_stride = rope_stride;
+  a.q_starts = q_starts;
+  a.kv_starts = kv_starts;
+  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  a.causal = causal;
+  a.out = out;
+  a.lse = lse;
+  a.num_tokens = num_tokens;
+  a.num_kv = num_kv;
+  a.num_heads = num_heads;
+  a.num_requests = num_requests;
+  return launched(latent::launch_prefill(a, stream), "latent-attention-expanded");
+}
+
+}  // extern "C"
