@@ -53,6 +53,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
   __shared__ PlanScan wave_sum[kPlanThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t wg = blockIdx.x, nwg = gridDim.x;
+  // this workgroup's first block (of kPlanThreads, dealt round-robin) that reaches item v or lies behind it
+  auto first_block = [&](int64_t v) {
+    const int64_t blk = v / kPlanThreads;
+    return blk + (uint32_t)(wg + nwg - (uint32_t)blk % (uint32_t)nwg) % (uint32_t)nwg;
+  };
   const int64_t page_mask = ((int64_t)1 << a.log2_page) - 1;
   const int64_t used = a.free_used ? a.free_used[0] : 0;
   int64_t tokens = 0, pages = 0;   // sums over the tiles before this one
@@ -114,9 +119,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
     }
     __syncthreads();
     // fresh pages of the tile's requests
-    for (int64_t blk = pages / kPlanThreads; blk * kPlanThreads < pages + tile_pages; ++blk) {
+    for (int64_t blk = first_block(pages); blk * kPlanThreads < pages + tile_pages; blk += nwg) {
       const int64_t p = blk * kPlanThreads + tid;
-      if (blk % nwg != wg || p < pages || p >= pages + tile_pages) continue;
+      if (p < pages || p >= pages + tile_pages) continue;
       const int r = find_start(p_start, n, p);
       const int64_t at = used + p;
       a.page_table[(base + r) * a.pages_per_row + had[r] + (p - p_start[r])] =
@@ -124,9 +129,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
     }
     // the tile's tokens
     const int64_t end = tokens + tile_tokens < a.num_tokens ? tokens + tile_tokens : a.num_tokens;
-    for (int64_t blk = tokens / kPlanThreads; blk * kPlanThreads < end; ++blk) {
+    for (int64_t blk = first_block(tokens); blk * kPlanThreads < end; blk += nwg) {
       const int64_t t = blk * kPlanThreads + tid;
-      if (blk % nwg != wg || t < tokens || t >= end) continue;
+      if (t < tokens || t >= end) continue;
       const int r = find_start(q_start, n, t);
       const int64_t pos = kv_len[r] + (t - q_start[r]);
       const int64_t col = pos >> a.log2_page;
@@ -146,9 +151,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
     __syncthreads();
   }
   // padding, and the totals
-  for (int64_t blk = tokens / kPlanThreads; blk * kPlanThreads < a.num_tokens; ++blk) {
+  for (int64_t blk = first_block(tokens); blk * kPlanThreads < a.num_tokens; blk += nwg) {
     const int64_t t = blk * kPlanThreads + tid;
-    if (blk % nwg != wg || t < tokens || t >= a.num_tokens) continue;
+    if (t < tokens || t >= a.num_tokens) continue;
     a.slot_map[t] = -1;
     a.positions[t] = -1;
   }
