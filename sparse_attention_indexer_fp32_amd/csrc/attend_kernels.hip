@@ -40,6 +40,7 @@ namespace {
 constexpr int kLatentSteps = kLatent / 32;   // a wave's 16 steps of the first product
 constexpr int kRopeSteps = kRope / 32;       // and 2 of the rotary part
 constexpr int kColBlocks = kLatent / 64;     // its 8 blocks of O^T
+constexpr int kReadsAhead = 3;               // matrix instructions whose LDS reads are in flight
 constexpr int kRowBytes = kLatent * 2;       // a row as bf16 in LDS
 constexpr int kRopeBytes = kRope * 2;
 constexpr int kTileLatent = kTileKeys * kRowBytes;
@@ -48,11 +49,27 @@ constexpr int kTileRope = kTileKeys * kRopeBytes;
 
 __device__ __attribute__((aligned(16))) const char kZeroRow[kRowBytes] = {};
 
-// One tile's rows as they are loaded.
-template <bool E4M3>
-struct Stage {
-  char latent[E4M3 ? kTileCodes : kTileLatent];
-  char rope[kTileRope];
+// A workgroup's LDS: a ring of stages (one tile's rows as they are loaded),
+// for E4M3 the current tile's rows as bf16 and the keys' scales, and the
+// waves' parts of the scores (E4M3 of up to two pairs: in the codes that have
+// been widened).  Sized so that two workgroups share a CU where they can, each
+// with one tile on its way while one is computed; where only one fits, two
+// tiles are on their way.
+template <int PAIRS, bool E4M3>
+struct Lds {
+  static constexpr int kWaves = 2 * PAIRS;
+  static constexpr int kLatentBytes = E4M3 ? kTileCodes : kTileLatent;
+  static constexpr int kStageBytes = kLatentBytes + kTileRope;
+  static constexpr int kAhead = PAIRS == 1 || (PAIRS == 2 && E4M3) ? 1 : 2;   // tiles on their way
+  static constexpr int kStages = kAhead + 1;
+  static constexpr bool kSwapInCodes = E4M3 && PAIRS <= 2;
+  static constexpr int kWide = kStages * kStageBytes;
+  static constexpr int kScales = kWide + (E4M3 ? kTileLatent : 0);            // a wave's own: 64 a stage
+  static constexpr int kEntries = kScales + (E4M3 ? kWaves * kStages * 256 : 0);   // a wave's own: two tiles
+  static constexpr int kSwap = kEntries + (kAhead > 1 ? kWaves * 2 * 256 : 0);
+  static constexpr int kBytes = kSwap + (kSwapInCodes ? 0 : kWaves * 4096);
+  // loads of rows a wave queues per tile, at least
+  static constexpr int kLoads = (E4M3 ? kTileKeys / 2 : kTileKeys) / kWaves + (kWaves <= 4 ? 4 / kWaves : 0);
 };
 
 // What a wave keeps of its 32 heads and its half of the values along a row of keys.
@@ -70,36 +87,64 @@ struct TokenKeys {
   const int32_t* list;       // the token's slots, or its request's pages
 };
 
+// Where the list's entry for this lane's key (lane % 32) of a tile is: its
+// slot, or its page.  Past the keys (of which there are some), the last one's.
 template <bool PAGED>
-__device__ __forceinline__ int tile_slot(const AttendArgs& a, const TokenKeys& tk, int64_t tile, int lane) {
-  const int64_t pos = tile * kTileKeys + (lane & (kTileKeys - 1));
-  int64_t slot = -1;
-  if (pos < tk.len) {
-    if (PAGED) {
-      const int64_t col = pos >> a.log2_page;
-      if (col < a.pages_per_row) {
-        const int64_t page = tk.list[col];
-        if (page >= 0) slot = (page << a.log2_page) + (pos & (((int64_t)1 << a.log2_page) - 1));
-      }
-    } else {
-      slot = tk.list[pos];
-    }
-  }
-  return slot >= 0 && slot < a.cache.num_slots ? (int)slot : -1;
+__device__ __forceinline__ const int32_t* entry_of(const AttendArgs& a, const TokenKeys& tk, int64_t tile) {
+  int64_t pos = tile * kTileKeys + (lane_here() & (kTileKeys - 1));
+  pos = pos < tk.len ? pos : tk.len - 1;
+  return tk.list + (PAGED ? pos >> a.log2_page : pos);      // (a token's keys are within its row of the page table)
 }
 
-// Queues the loads of a tile's rows; `slots`: lane i (mod 32) holds key i's.
+// The slot of that key, or -1 when it selects nothing.
+template <bool PAGED>
+__device__ __forceinline__ int slot_of(const AttendArgs& a, const TokenKeys& tk, int entry, int64_t tile) {
+  const int64_t pos = tile * kTileKeys + (lane_here() & (kTileKeys - 1));
+  int64_t slot = entry;
+  if (PAGED && entry >= 0) slot = ((int64_t)entry << a.log2_page) + (pos & (((int64_t)1 << a.log2_page) - 1));
+  return pos < tk.len && slot >= 0 && slot < a.cache.num_slots ? (int)slot : -1;
+}
+
+// Tiles of [first, last) up to the last one that has a selected key; wave-uniform.
+__device__ __forceinline__ int64_t selected_tiles(const AttendArgs& a, const TokenKeys& tk, int64_t first, int64_t last,
+                                                  int lane) {
+  const int64_t begin = first * kTileKeys, stop = last * kTileKeys < tk.len ? last * kTileKeys : tk.len;
+  // from the end, in blocks: most rows are full
+  for (int64_t base = stop; base > begin; base -= 256) {
+    uint64_t any[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = base - 1 - i * 64 - lane;
+      const int s = at >= begin ? tk.list[at] : -1;
+      any[i] = __ballot(s >= 0 && s < a.cache.num_slots);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (any[i]) return (base - 1 - i * 64 - (int64_t)__builtin_ctzll(any[i])) / kTileKeys - first + 1;
+  }
+  return 0;
+}
+
+// A slot's row; zeros for a slot below 0.  (Selected, not branched on: a tile
+// takes 32 of them.)
+__device__ __forceinline__ const char* row_at(const char* base, int64_t stride, int slot) {
+  return (slot < 0 ? kZeroRow : base) + (int64_t)(slot < 0 ? 0 : slot) * stride;
+}
+
+// Queues the loads of a tile's rows into the stage at LDS address `lds`;
+// `slots`: lane i (mod 32) holds key i's.
 template <int NW, bool E4M3>
-__device__ __forceinline__ void load_tile(const Cache& c, int slots, Stage<E4M3>& st, int lane, int wave) {
+__device__ __forceinline__ void load_tile(const Cache& c, int slots, uint32_t lds, int wave) {
+  const int lane = lane_here();
   if (E4M3) {
     constexpr int kEach = kTileKeys / 2 / NW;   // two rows an instruction
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int pair = wave * kEach + i;
       const int s0 = __builtin_amdgcn_readlane(slots, 2 * pair), s1 = __builtin_amdgcn_readlane(slots, 2 * pair + 1);
-      const char* r0 = s0 >= 0 ? c.latent + (int64_t)s0 * c.latent_stride : kZeroRow;
-      const char* r1 = s1 >= 0 ? c.latent + (int64_t)s1 * c.latent_stride : kZeroRow;
-      load_to_lds((lane < 32 ? r0 : r1) + (lane & 31) * 16, st.latent + pair * 2 * kLatent);
+      const char* r0 = row_at(c.latent, c.latent_stride, s0);
+      const char* r1 = row_at(c.latent, c.latent_stride, s1);
+      queue_to_lds((lane < 32 ? r0 : r1) + (lane & 31) * 16, lds + pair * 2 * kLatent);
     }
   } else {
     constexpr int kEach = kTileKeys / NW;
@@ -107,25 +152,26 @@ __device__ __forceinline__ void load_tile(const Cache& c, int slots, Stage<E4M3>
     for (int i = 0; i < kEach; ++i) {
       const int key = wave * kEach + i;
       const int s = __builtin_amdgcn_readlane(slots, key);
-      const char* row = s >= 0 ? c.latent + (int64_t)s * c.latent_stride : kZeroRow;
-      load_to_lds(row + (lane ^ swizzle(key)) * 16, st.latent + key * kRowBytes);
+      const char* row = row_at(c.latent, c.latent_stride, s);
+      queue_to_lds(row, (uint32_t)(lane ^ swizzle(key)) * 16, lds + key * kRowBytes);
     }
   }
+  lds += E4M3 ? kTileCodes : kTileLatent;
   constexpr int kRopeEach = NW < 4 ? 4 / NW : 1;   // eight rows an instruction
   if (NW > 4 && wave >= 4) return;
 #pragma unroll
   for (int i = 0; i < kRopeEach; ++i) {
     const int group = wave * kRopeEach + i;
-    const int key = group * 8 + (lane >> 3);
-    const int s = __shfl(slots, key);
-    const char* row = s >= 0 ? c.rope + (int64_t)s * c.rope_stride : kZeroRow;
-    load_to_lds(row + ((lane ^ key) & 7) * 16, st.rope + group * 8 * kRopeBytes);
+    const int s = __shfl(slots, group * 8 + (lane >> 3));
+    const char* row = row_at(c.rope, c.rope_stride, s);
+    queue_to_lds(row + ((lane ^ (lane >> 3)) & 7) * 16, lds + group * 8 * kRopeBytes);
   }
 }
 
 // E4M3 rows of a stage as bf16 rows (exact), in the layout bf16 rows are loaded in.
 template <int NW>
-__device__ __forceinline__ void widen_tile(const char* codes, char* lat, int tid) {
+__device__ __forceinline__ void widen_tile(const char* codes, char* lat, int wave) {
+  const int tid = wave * 64 + lane_here();
 #pragma unroll
   for (int i = 0; i < kTileCodes / 16 / (64 * NW); ++i) {
     const int at = i * 64 * NW + tid;
@@ -147,39 +193,50 @@ __device__ __forceinline__ void widen_tile(const char* codes, char* lat, int tid
   }
 }
 
+// A lane's LDS offsets within a tile, for its wave's half of the values.  The
+// other offsets differ from these in bits that the swizzle only flips: chunk
+// 2 k + hb in bits 5 to 7 (key, rope), column block cb in bits 6 and 7
+// (value).  They are formed where they are read: as registers of their own they
+// would push Q and O^T out.
+struct TileReads {
+  int key;      // row lane % 32, 16-byte chunk hb
+  int rope;
+  int value;    // transposed reads of rows 4 hb + 0..3, column block 0
+};
+
+__device__ __forceinline__ TileReads tile_reads(int half, int lane) {
+  const int i = lane & 31, hb = lane >> 5, j = lane & 15, quarter = (lane >> 4) & 1;
+  const int key = 4 * hb + (j >> 2);
+  TileReads t;
+  t.key = i * kRowBytes + half * (kRowBytes / 2) + ((hb ^ swizzle(i)) << 4);
+  t.rope = i * kRopeBytes + ((((2 * half * kRopeSteps + hb) ^ i) & 7) << 4);
+  t.value = key * kRowBytes + half * (kRowBytes / 2) + (((2 * quarter + ((j & 3) >> 1)) ^ swizzle(key)) << 4) + (j & 1) * 8;
+  return t;
+}
+
 // A wave's part of a tile's scores: its half of the values.  scales (E4M3):
 // each key's scale.
 template <bool E4M3>
 __device__ __forceinline__ f32x16 score_tile(const HeadState& st, const char* lat, const char* rope,
-                                             const float* scales, int half, int lane) {
-  const int i = lane & 31, hb = lane >> 5;
+                                             const float* scales, const TileReads& at, int lane) {
+  const int hb = lane >> 5;
   f32x16 s = {};
-  {
-    const char* row = lat + i * kRowBytes + half * (kRowBytes / 2);
-    const int sw = swizzle(i);
+  const int key = here(at.key);
+  auto read = [&](int k) {
+    const char* from = k < kLatentSteps ? lat + (k >> 3) * 256 + (key ^ ((k & 7) << 5)) : rope + (at.rope ^ ((k - kLatentSteps) << 5));
+    return *reinterpret_cast<const bf16x8*>(from);
+  };
+  run_ahead<kLatentSteps + kRopeSteps, kReadsAhead>(read, [&](int k, bf16x8 rows) {
+    if (E4M3 && k == kLatentSteps) {
 #pragma unroll
-    for (int k = 0; k < kLatentSteps; ++k) {
-      const bf16x8 key = *reinterpret_cast<const bf16x8*>(row + (k >> 3) * 256 + (((2 * (k & 7) + hb) ^ sw) << 4));
-      s = mfma(key, st.q[k], s);
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[4 * g + e] *= sc[e];
+      }
     }
-  }
-  if (E4M3) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[4 * g + e] *= sc[e];
-    }
-  }
-  {
-    const char* row = rope + i * kRopeBytes;
-#pragma unroll
-    for (int k = 0; k < kRopeSteps; ++k) {
-      const bf16x8 key =
-          *reinterpret_cast<const bf16x8*>(row + (((2 * (half * kRopeSteps + k) + hb) ^ i) & 7) * 16);
-      s = mfma(key, st.q[kLatentSteps + k], s);
-    }
-  }
+    s = mfma(rows, st.q[k], s);
+  });
   return s;
 }
 
@@ -187,19 +244,18 @@ __device__ __forceinline__ f32x16 score_tile(const HeadState& st, const char* la
 // mask: the tile's selected keys.
 template <bool E4M3>
 __device__ __forceinline__ void weigh_tile(HeadState& st, f32x16 s, const char* lat, const float* scales,
-                                           uint32_t mask, float scale_log2, int half, int lane) {
+                                           uint32_t mask, float scale_log2, const TileReads& at, int lane) {
   const int hb = lane >> 5;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) s[r] *= scale_log2;
   if (mask != 0xFFFFFFFFu) {
+    const uint32_t own = mask >> (4 * hb);
 #pragma unroll
     for (int r = 0; r < 16; ++r)
-      if (!((mask >> acc_row(r, hb)) & 1)) s[r] = -INFINITY;
+      if (!((own >> acc_row(r, 0)) & 1)) s[r] = -INFINITY;
   }
   float top = s[0];
 #pragma unroll
   for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-  top = fmaxf(top, other_half(top, lane));
+  top = fmaxf(top, other_half(top, lane)) * scale_log2;
   if (__any(top > st.m + kLazy)) {
     const float m = fmaxf(st.m, top);
     const float f = __builtin_amdgcn_exp2f(st.m - m);
@@ -219,27 +275,20 @@ __device__ __forceinline__ void weigh_tile(HeadState& st, f32x16 s, const char* 
     if (E4M3) sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float w = __builtin_amdgcn_exp2f(s[4 * g + e] - st.m);
+      const float w = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], scale_log2, -st.m));
       st.l += w;
       p[g >> 1][(g & 1) * 4 + e] = (__bf16)(E4M3 ? w * sc[e] : w);
     }
   }
-  const int j = lane & 15, quarter = (lane >> 4) & 1;
-  lat += half * (kRowBytes / 2);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-#pragma unroll
-    for (int cb = 0; cb < kColBlocks; ++cb) {
-      const int chunk = (cb & 3) * 4 + 2 * quarter + ((j & 3) >> 1);
-      bf16x4 v[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int key = 16 * k + 8 * e + 4 * hb + (j >> 2);
-        v[e] = read_tr(lat + key * kRowBytes + (cb >> 2) * 256 + ((chunk ^ swizzle(key)) << 4) + (j & 1) * 8);
-      }
-      st.o[cb] = mfma(join8(v[0], v[1]), p[k], st.o[cb]);
-    }
-  }
+  const int value = here(at.value);
+  run_ahead<2 * kColBlocks, kReadsAhead>(
+      [&](int i) {
+        // rows 8 further swizzle with bit 3 flipped: the offset of column block cb ^ 2
+        const int k = i / kColBlocks, cb = i % kColBlocks;
+        const char* v = lat + 16 * k * kRowBytes + (cb >> 2) * 256;
+        return join8(read_tr(v + (value ^ ((cb & 3) << 6))), read_tr(v + 8 * kRowBytes + (value ^ (((cb & 3) ^ 2) << 6))));
+      },
+      [&](int i, bf16x8 cols) { st.o[i % kColBlocks] = mfma(cols, p[i / kColBlocks], st.o[i % kColBlocks]); });
 }
 
 // Last of the n ascending starts at or below v, 64 at a time; wave-uniform.
@@ -322,11 +371,9 @@ __device__ void plan_split(const AttendArgs& a, SplitPlan& plan, int tid) {
 template <int PAIRS, bool E4M3, bool PAGED>
 __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
   constexpr int NW = 2 * PAIRS;
-  __shared__ __attribute__((aligned(16))) Stage<E4M3> stage0, stage1;
-  __shared__ __attribute__((aligned(16))) char wide[E4M3 ? kTileLatent : 16];
-  __shared__ __attribute__((aligned(16))) float scales[NW][kTileKeys];
-  __shared__ __attribute__((aligned(16))) float swap[NW][16 * 64];
-  __shared__ SplitPlan plan;
+  using L = Lds<PAIRS, E4M3>;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pair = wave >> 1, half = wave & 1;
@@ -335,30 +382,36 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
   const bool live_wave = head0 < a.num_heads;
   const bool split = a.wgs > 0;
 
-  // this workgroup's tiles [lo, hi) of all tokens' tiles, beginning in token t
-  int64_t lo, hi, t, total = 0;
+  // this workgroup's tiles [lo, hi) of all tokens' tiles, beginning in token
+  // t, whose first tile is number `start` and whose request is b
+  int64_t lo = 0, hi = INT64_MAX, t, start = 0, total = 0, b = 0;
   int wgs = 1;
   const int64_t k_tiles = token_tiles(a.k);
   if (split) {
     if (PAGED) {
+      SplitPlan& plan = *reinterpret_cast<SplitPlan*>(lds);
       plan_split<NW>(a, plan, tid);
-      total = plan.start[a.num_tokens];
-    } else {
-      total = a.num_tokens * k_tiles;
-    }
-    wgs = (int)(a.wgs < total ? a.wgs : total);
-    if ((int)blockIdx.x >= wgs) return;
-    lo = total * blockIdx.x / wgs;
-    hi = total * (blockIdx.x + 1) / wgs;
-    if (PAGED) {
+      total = __builtin_amdgcn_readfirstlane(plan.start[a.num_tokens]);
+      wgs = (int)(a.wgs < total ? a.wgs : total);
+      if ((int)blockIdx.x >= wgs) return;
+      lo = total * blockIdx.x / wgs;
+      hi = total * (blockIdx.x + 1) / wgs;
       int l = 0, h = a.num_tokens;
       while (h - l > 1) {
         const int mid = (l + h) >> 1;
         if (plan.start[mid] <= lo) l = mid; else h = mid;
       }
       t = __builtin_amdgcn_readfirstlane(l);
+      start = __builtin_amdgcn_readfirstlane(plan.start[t]);
+      b = __builtin_amdgcn_readfirstlane((int)plan.request[t]);
     } else {
+      total = a.num_tokens * k_tiles;
+      wgs = (int)(a.wgs < total ? a.wgs : total);
+      if ((int)blockIdx.x >= wgs) return;
+      lo = total * blockIdx.x / wgs;
+      hi = total * (blockIdx.x + 1) / wgs;
       t = lo / k_tiles;
+      start = t * k_tiles;
     }
   } else {
     // neighbouring tokens select neighbouring rows: each XCD (workgroups are
@@ -367,32 +420,25 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
     t = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((blockIdx.x >> 3) >= per || t >= a.num_tokens) return;
     if (PAGED && t >= (int64_t)a.q_starts[a.num_requests]) return;
-    lo = 0;
-    hi = INT64_MAX;
+    if (PAGED) b = count_starts(a.q_starts, a.num_requests, t, lane);
   }
 
+  const TileReads reads = tile_reads(half, lane);
+  const float scale_log2 = fabsf(a.scale_log2);
   while (lo < hi) {
     // the part [first, last) of token t's n tiles
     TokenKeys tk;
     tk.token = t;
-    int64_t first = lo, last = hi, n;
     if (PAGED) {
-      const int64_t b = split ? (int64_t)__builtin_amdgcn_readfirstlane((int)plan.request[t])
-                              : count_starts(a.q_starts, a.num_requests, t, lane);
+      while (t >= (int64_t)a.q_starts[b + 1]) ++b;
       tk.len = token_len(a, t, b);
       tk.list = a.page_table + b * a.pages_per_row;
     } else {
       tk.len = a.k;
       tk.list = a.indices + t * a.k;
     }
-    n = token_tiles(tk.len);
-    int64_t start = 0;
-    if (split) {
-      start = PAGED ? (int64_t)__builtin_amdgcn_readfirstlane(plan.start[t]) : t * k_tiles;
-      first = lo - start;
-      last = hi - start;
-    }
-    if (last > n) last = n;
+    const int64_t n = token_tiles(tk.len);
+    const int64_t first = lo - start, last = hi - start < n ? hi - start : n;
     const bool whole = first == 0 && last == n;
 
     HeadState st;
@@ -401,60 +447,102 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
 #pragma unroll
     for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x16{};
     {
+      // a negative scale goes into the signs of q: the largest product is then the largest score
+      const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
       const uint16_t* q = a.q + t * a.q_token_stride + (int64_t)head * a.q_head_stride + hb * 8;
 #pragma unroll
       for (int k = 0; k < kLatentSteps + kRopeSteps; ++k) {
         const int at = k < kLatentSteps ? (half * kLatentSteps + k) * 16
                                         : kLatent + (half * kRopeSteps + k - kLatentSteps) * 16;
-        st.q[k] = bf16x8{};
-        if (head < a.num_heads) st.q[k] = *reinterpret_cast<const bf16x8*>(q + at);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (head < a.num_heads) v = *reinterpret_cast<const uint4*>(q + at);
+        st.q[k] = __builtin_bit_cast(bf16x8, make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign));
       }
     }
 
-    int slots = tile_slot<PAGED>(a, tk, first, lane);           // of the tile being loaded
-    lds_barrier();                                              // the last part's reads are done
-    load_tile<NW, E4M3>(a.cache, slots, stage0, lane, wave);
-    float scale = E4M3 && slots >= 0 ? a.cache.scale[slots] : 0.f;
-    int next = first + 1 < last ? tile_slot<PAGED>(a, tk, first + 1, lane) : -1;
-
-    auto step = [&](int64_t tile, Stage<E4M3>& cur, Stage<E4M3>& nxt) {
-      const uint32_t mask = (uint32_t)__ballot(slots >= 0);
-      if (E4M3 && lane < kTileKeys) scales[wave][lane] = scale;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      lds_barrier();            // every wave's rows are there, and nobody reads the other stage any more
-      if (tile + 1 < last) {
-        slots = next;
-        load_tile<NW, E4M3>(a.cache, slots, nxt, lane, wave);
-        scale = E4M3 && slots >= 0 ? a.cache.scale[slots] : 0.f;
-        next = tile + 2 < last ? tile_slot<PAGED>(a, tk, tile + 2, lane) : -1;
-      }
-      if (mask == 0) return;
+    // Tiles past the part's last selected key hold nothing (a short row's tail).
+    const int64_t end = PAGED ? (tk.len > 0 ? last : first) : first + selected_tiles(a, tk, first, last, lane);
+    // The ring: tile i is in stage (i - first) % kStages; masks[d], the
+    // selected keys of the tile d after the one being computed.  A tile's list
+    // entries are loaded one tile before its rows.  With two tiles on their
+    // way, entries and scales too are loaded into LDS, so that no load in the
+    // loop is the compiler's to wait for.
+    uint32_t masks[L::kAhead + 1];
+    int entry = 0;                        // kAhead == 1: of the tile to be queued next
+    float scale = 0.f;                    // and lane i: the scale of key i of the tile queued last
+    int into = 0;                         // the stage of the tile to be queued next
+    char* own_entries = lds + L::kEntries + wave * 512;
+    float* scales = reinterpret_cast<float*>(lds + L::kScales + wave * L::kStages * 256);
+    lds_barrier();                        // the last part's reads are done
+    auto load_entries = [&](int64_t tile) {
+      const int32_t* at = entry_of<PAGED>(a, tk, tile);
+      if (L::kAhead > 1)
+        queue_word_to_lds(at, lds_base + L::kEntries + wave * 512 + (uint32_t)(tile & 1) * 256);
+      else
+        entry = *at;
+    };
+    auto queue = [&](int64_t tile, uint32_t& mask) {
+      if (L::kAhead > 1) entry = *reinterpret_cast<const int*>(own_entries + (tile & 1) * 256 + lane_here() * 4);
+      const int slot = slot_of<PAGED>(a, tk, entry, tile);
+      mask = (uint32_t)__ballot(slot >= 0);
+      if (tile + 1 < end) load_entries(tile + 1);
       if (E4M3) {
-        widen_tile<NW>(cur.latent, wide, tid);
+        const float* at = slot >= 0 ? a.cache.scale + slot : reinterpret_cast<const float*>(kZeroRow);
+        if (L::kAhead > 1)
+          queue_word_to_lds(at, lds_base + L::kScales + (wave * L::kStages + into) * 256);
+        else
+          scale = *at;
+      }
+      load_tile<NW, E4M3>(a.cache, slot, lds_base + into * L::kStageBytes, wave);
+      into = into + 1 < L::kStages ? into + 1 : 0;
+    };
+    if (first < end) {
+      load_entries(first);
+      wait_loads<0>();
+    }
+#pragma unroll
+    for (int d = 0; d < L::kAhead; ++d) {
+      masks[d] = 0;
+      if (first + d < end) {
+        queue(first + d, masks[d]);
+        if (d + 1 < L::kAhead) wait_loads<L::kLoads>();        // the next entries
+      }
+    }
+    int from = 0;                         // the stage of the tile being computed
+    for (int64_t tile = first; tile < end; ++tile) {
+      if (L::kAhead > 1 && tile + 1 < end)
+        wait_loads<L::kLoads>();          // all but the next tile's rows
+      else
+        wait_loads<0>();
+      if (E4M3 && L::kAhead == 1) scales[from * 64 + lane_here()] = scale;
+      lds_barrier();            // every wave's rows are there, and nobody reads the stage before any more
+      masks[L::kAhead] = 0;
+      if (tile + L::kAhead < end) queue(tile + L::kAhead, masks[L::kAhead]);
+      const uint32_t mask = masks[0];
+#pragma unroll
+      for (int d = 0; d < L::kAhead; ++d) masks[d] = masks[d + 1];
+      char* stage = lds + from * L::kStageBytes;
+      const float* sc = scales + from * 64;
+      from = from + 1 < L::kStages ? from + 1 : 0;
+      const char* lat = stage;
+      if (E4M3) {
+        widen_tile<NW>(stage, lds + L::kWide, wave);
+        lat = lds + L::kWide;
         lds_barrier();
       }
-      const char* lat = E4M3 ? wide : cur.latent;
-      f32x16 s = {};
-      if (live_wave) {
-        s = score_tile<E4M3>(st, lat, cur.rope, scales[wave], half, lane);
+      float* swap = reinterpret_cast<float*>(L::kSwapInCodes ? stage : lds + L::kSwap) + lane * 4;
+      f32x16 s = score_tile<E4M3>(st, lat, stage + L::kLatentBytes, sc, reads, lane);
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<f32x4*>(&swap[wave][g * 256 + lane * 4]) = f32x4{s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]};
-      }
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4*>(swap + wave * 1024 + g * 256) = f32x4{s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]};
       lds_barrier();
-      if (live_wave) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4 o = *reinterpret_cast<const f32x4*>(&swap[wave ^ 1][g * 256 + lane * 4]);
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 o = *reinterpret_cast<const f32x4*>(swap + (wave ^ 1) * 1024 + g * 256);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[4 * g + e] += o[e];
-        }
-        weigh_tile<E4M3>(st, s, lat, scales[wave], mask, a.scale_log2, half, lane);
+        for (int e = 0; e < 4; ++e) s[4 * g + e] += o[e];
       }
-    };
-    for (int64_t tile = first; tile < last; tile += 2) {
-      step(tile, stage0, stage1);
-      if (tile + 1 < last) step(tile + 1, stage1, stage0);
+      weigh_tile<E4M3>(st, s, lat, sc, mask, scale_log2, reads, lane);
     }
 
     // this lane's head: its sum is spread over the two half-waves
@@ -505,6 +593,7 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
     }
     if (!split) return;
     lo = start + last;
+    start += n;
     ++t;
   }
 }
@@ -555,11 +644,13 @@ template <int PAIRS, bool E4M3>
 hipError_t launch(const AttendArgs& a, hipStream_t stream) {
   const unsigned x = a.wgs > 0 ? (unsigned)a.wgs : (unsigned)(((int64_t)a.num_tokens + 7) / 8 * 8);
   const dim3 grid(x, (unsigned)head_blocks(a.num_heads, PAIRS)), block(128 * PAIRS);
-  if (a.indices)
-    hipLaunchKernelGGL((attend_kernel<PAIRS, E4M3, false>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((attend_kernel<PAIRS, E4M3, true>), grid, block, 0, stream, a);
-  hipError_t e = hipGetLastError();
+  constexpr int kLds = Lds<PAIRS, E4M3>::kBytes;
+  static_assert(kLds <= 160 * 1024 && sizeof(SplitPlan) <= (size_t)kLds, "LDS of a workgroup");
+  auto* kernel = a.indices ? attend_kernel<PAIRS, E4M3, false> : attend_kernel<PAIRS, E4M3, true>;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a);
+  e = hipGetLastError();
   if (e != hipSuccess || a.wgs == 0) return e;
   hipLaunchKernelGGL(join_kernel<PAIRS>, dim3((unsigned)a.num_tokens, (unsigned)((a.num_heads + 31) / 32), 2 * kColBlocks),
                      dim3(256), 0, stream, a);

@@ -85,6 +85,12 @@ topk_status_t check_cache(const void* latent, int64_t latent_stride, const uint1
   return TOPK_SUCCESS;
 }
 
+// The kernels' scale: in log2 units, and not quite 0, which would make 0 * -inf
+// of a masked score (2^-100 leaves every score as good as 0).
+float scale_log2(float softmax_scale) {
+  return softmax_scale == 0.f ? 0x1p-100f : softmax_scale * 1.44269504088896340736f;
+}
+
 // Workgroups that share the tiles of a launch of absorbed attention, or 0 for one
 // workgroup per token.  Two workgroups of up to 64 heads fit a CU, one of 128.
 int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, int32_t num_requests) {
@@ -302,7 +308,7 @@ topk_status_t latent_attention(const uint16_t* q, int64_t q_token_stride, int64_
   // with k = 0 nothing is read through it, but it tells the two forms apart
   a.indices = indices ? indices : reinterpret_cast<const int32_t*>(q);
   a.k = k;
-  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  a.scale_log2 = scale_log2(softmax_scale);
   a.out = out;
   a.lse = lse;
   a.num_tokens = num_tokens;
@@ -339,7 +345,7 @@ topk_status_t latent_attention_paged(const uint16_t* q, int64_t q_token_stride, 
   a.q_starts = q_starts;
   a.pages_per_row = pages_per_row;
   a.num_requests = num_requests;
-  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  a.scale_log2 = scale_log2(softmax_scale);
   a.out = out;
   a.lse = lse;
   a.num_tokens = num_tokens;
@@ -383,7 +389,7 @@ topk_status_t latent_attention_expanded(const uint16_t* q, int64_t q_token_strid
   a.rope_stride = rope_stride;
   a.q_starts = q_starts;
   a.kv_starts = kv_starts;
-  a.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  a.scale_log2 = scale_log2(softmax_scale);
   a.causal = causal;
   a.out = out;
   a.lse = lse;

@@ -54,6 +54,32 @@ __device__ __forceinline__ void load_to_lds(const char* src, char* dst) {
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
+// The same, as instructions that the compiler does not count among its own
+// loads: it puts a wait for all loads in front of an LDS read that may follow a
+// load into the same array, and a ring of stages in one array is such.  The
+// caller waits (wait_loads) and passes a barrier before it reads the bytes.
+// lds: byte address in LDS.
+__device__ __forceinline__ void queue_to_lds(const char* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(offset), "s"(base), "s"(lds) : "m0", "memory");
+}
+__device__ __forceinline__ void queue_to_lds(const char* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(src), "s"(lds) : "m0", "memory");
+}
+
+// 4 bytes per lane, to lds + 4 * lane.
+__device__ __forceinline__ void queue_word_to_lds(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :: "v"(src), "s"(lds) : "m0", "memory");
+}
+
+// Waits until at most N of this wave's vector loads are in flight (they complete in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+
 // Workgroup barrier that leaves vector loads in flight (they are waited for
 // by count where their data is used).  LDS accesses before it have completed.
 __device__ __forceinline__ void lds_barrier() {
@@ -62,10 +88,43 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// A run of N matrix instructions whose LDS reads are issued D instructions
+// ahead: read(i) gives step i's operand, use(i, operand) multiplies it.  The
+// compiler, left alone with few registers to spare, places each read right in
+// front of its use, and every matrix instruction then waits for the LDS; the
+// scheduling barriers keep the order written here.
+template <int N, int D, typename Read, typename Use>
+__device__ __forceinline__ void run_ahead(Read read, Use use) {
+  decltype(read(0)) held[D];
+#pragma unroll
+  for (int i = 0; i < D; ++i) held[i] = read(i);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    use(i, held[i % D]);
+    if (i + D < N) held[i % D] = read(i + D);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // Value of the other half-wave's lane (l ^ 32).
 __device__ __forceinline__ float other_half(float v, int lane) {
   const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(lane < 32 ? sw[1] : sw[0]);
+}
+
+// The same value, computed where it is used: keeps what a rare path derives
+// from it out of registers that the common path needs.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The lane's number, worked out where it is used (nothing is kept in a register for it).
+__device__ __forceinline__ int lane_here() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;

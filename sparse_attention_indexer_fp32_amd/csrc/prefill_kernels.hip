@@ -36,8 +36,6 @@ constexpr int kHeadSteps = kHead / 16;       // 8 steps of the first product
 constexpr int kRopeSteps = kRope / 16;       // and 4 of the rotary part
 constexpr int kColBlocks = kHead / 32;       // 4 blocks of O^T
 
-__device__ __attribute__((aligned(16))) const char kZeroRow[kUpBytes] = {};
-
 struct Stage {
   char up[kKeys * kUpBytes];
   char rope[kKeys * kRopeBytes];
@@ -88,26 +86,40 @@ __device__ __forceinline__ bool find_block(const PrefillArgs& a, int64_t index, 
   return false;
 }
 
-// Queues the loads of a tile's rows from key j0 on; rows past nk are zeros.
-__device__ __forceinline__ void load_tile(const PrefillArgs& a, const Block& blk, int64_t head, int64_t j0, Stage& st,
-                                          int lane, int wave) {
+// Where a lane's loads of a tile come from: byte offsets from the tile's first
+// rows, the same for every whole tile.
+struct TileLoads {
+  uint32_t up[kKeys / 2 / kWaves];     // two rows an instruction
+  uint32_t rope[kKeys / 8 / kWaves];   // eight rotary keys an instruction
+};
+
+// Rows at or past `rows` are replaced by the last row before: whatever it
+// holds, its weight is masked.
+__device__ __forceinline__ TileLoads tile_loads(const PrefillArgs& a, int rows, int lane, int wave) {
+  TileLoads t;
 #pragma unroll
   for (int i = 0; i < kKeys / 2 / kWaves; ++i) {
-    const int pair = wave * (kKeys / 2 / kWaves) + i;   // two rows an instruction
-    const int key = 2 * pair + (lane >> 5);
-    const int p = lane & 31;
-    const char* row = j0 + key < blk.nk
-        ? reinterpret_cast<const char*>(a.kv + (blk.k0 + j0 + key) * a.kv_token_stride + head * a.kv_head_stride)
-        : kZeroRow;
-    load_to_lds(row + (p ^ swizzle(key)) * 16, st.up + pair * 2 * kUpBytes);
+    const int key = 2 * (wave * (kKeys / 2 / kWaves) + i) + (lane >> 5);
+    const int row = key < rows ? key : rows - 1;
+    t.up[i] = (uint32_t)row * (uint32_t)(a.kv_token_stride * 2) + (uint32_t)(((lane & 31) ^ swizzle(key)) * 16);
   }
 #pragma unroll
   for (int i = 0; i < kKeys / 8 / kWaves; ++i) {
-    const int group = wave * (kKeys / 8 / kWaves) + i;  // eight rotary keys an instruction
-    const int key = group * 8 + (lane >> 3);
-    const char* row = j0 + key < blk.nk ? reinterpret_cast<const char*>(a.rope + (blk.k0 + j0 + key) * a.rope_stride) : kZeroRow;
-    load_to_lds(row + ((lane ^ key) & 7) * 16, st.rope + group * 8 * kRopeBytes);
+    const int key = 8 * (wave * (kKeys / 8 / kWaves) + i) + (lane >> 3);
+    const int row = key < rows ? key : rows - 1;
+    t.rope[i] = (uint32_t)row * (uint32_t)(a.rope_stride * 2) + (uint32_t)(((lane ^ key) & 7) * 16);
   }
+  return t;
+}
+
+// Queues the loads of the tile whose first rows are at up and rope.
+__device__ __forceinline__ void load_tile(const char* up, const char* rope, const TileLoads& t, Stage& st, int wave) {
+#pragma unroll
+  for (int i = 0; i < kKeys / 2 / kWaves; ++i)
+    load_to_lds(up + t.up[i], st.up + (wave * (kKeys / 2 / kWaves) + i) * 2 * kUpBytes);
+#pragma unroll
+  for (int i = 0; i < kKeys / 8 / kWaves; ++i)
+    load_to_lds(rope + t.rope[i], st.rope + (wave * (kKeys / 8 / kWaves) + i) * 8 * kRopeBytes);
 }
 
 struct RowState {
@@ -117,35 +129,97 @@ struct RowState {
   float l;      // this lane's part of the sum
 };
 
-// One tile for a wave's 32 queries.  limit: the lane's query attends the
-// tile's keys below it (any value; at least kKeys: all).
-__device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, int limit, bool masked, float scale_log2,
-                                            int lane) {
-  const int i = lane & 31, hb = lane >> 5;
+// A lane's LDS offsets within a tile.
+struct TileReads {
+  uint32_t key[kHeadSteps];            // of row lane % 32, 16-byte chunk 2 k + hb
+  uint32_t rope[kRopeSteps];
+  uint32_t value[kColBlocks];          // transposed reads of rows 4 hb + 0..3, column block cb
+};
+
+__device__ __forceinline__ TileReads tile_reads(int lane) {
+  TileReads t;
+  const int i = lane & 31, hb = lane >> 5, j = lane & 15, quarter = (lane >> 4) & 1;
+#pragma unroll
+  for (int k = 0; k < kHeadSteps; ++k) t.key[k] = i * kUpBytes + (((2 * k + hb) ^ swizzle(i)) << 4);
+#pragma unroll
+  for (int k = 0; k < kRopeSteps; ++k) t.rope[k] = i * kRopeBytes + ((((2 * k + hb) ^ i) & 7) << 4);
+  const int key = 4 * hb + (j >> 2);
+#pragma unroll
+  for (int cb = 0; cb < kColBlocks; ++cb)
+    t.value[cb] = key * kUpBytes + kUpBytes / 2 + (((cb * 4 + 2 * quarter + ((j & 3) >> 1)) ^ swizzle(key)) << 4) + (j & 1) * 8;
+  return t;
+}
+
+// Whether a tile's values hold an infinity or a NaN (the same answer in every lane).
+__device__ __forceinline__ bool values_not_finite(const Stage& t, int lane) {
+  bool bad = false;
+#pragma unroll 4
+  for (int at = lane; at < kKeys * 16; at += 64) {
+    const uint4 v = *reinterpret_cast<const uint4*>(t.up + (at >> 4) * kUpBytes + kUpBytes / 2 + (at & 15) * 16);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      bad = bad || (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
+  }
+  return __any(bad);
+}
+
+// The second product of a masked tile whose values are not all finite: a
+// matrix product would bring 0 * inf = NaN into rows that do not attend the
+// key, so each key is added where it is attended only.
+__device__ __forceinline__ void add_values_one_by_one(f32x16 (&o)[kColBlocks], const f32x16 (&w)[2],
+                                                                const Stage& t, int limit, int lane) {
+  const int hb = lane >> 5;
+#pragma unroll 1
+  for (int key = 0; key < kKeys; ++key) {
+    // the weight of this lane's query for the key sits in one half-wave
+    float own = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (32 * kb + acc_row(r, hb) == key) own = w[kb][r];
+    const float p = own + other_half(own, lane);
+    if (key >= limit) continue;
+    const int row = here(hb);
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int col = cb * 32 + acc_row(r, row);
+        const char* at = t.up + key * kUpBytes + kUpBytes / 2 + (((col >> 3) ^ swizzle(key)) << 4) + (col & 7) * 2;
+        o[cb][r] = fmaf((float)(__bf16)p, (float)*reinterpret_cast<const __bf16*>(at), o[cb][r]);
+      }
+  }
+}
+
+// One tile for a wave's 32 queries.  MASKED: the lane's query attends the
+// tile's keys below `limit` only.
+template <bool MASKED>
+__device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const TileReads& at, int limit,
+                                            float scale_log2, int lane) {
+  const int hb = lane >> 5;
   f32x16 s[2];
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
     s[kb] = f32x16{};
-    const char* up = t.up + (32 * kb + i) * kUpBytes;
-    const char* rope = t.rope + (32 * kb + i) * kRopeBytes;
-    const int sw = swizzle(i);
 #pragma unroll
     for (int k = 0; k < kHeadSteps; ++k)
-      s[kb] = mfma(*reinterpret_cast<const bf16x8*>(up + (((2 * k + hb) ^ sw) << 4)), st.q[k], s[kb]);
+      s[kb] = mfma(*reinterpret_cast<const bf16x8*>(t.up + 32 * kb * kUpBytes + at.key[k]), st.q[k], s[kb]);
 #pragma unroll
     for (int k = 0; k < kRopeSteps; ++k)
-      s[kb] = mfma(*reinterpret_cast<const bf16x8*>(rope + ((((2 * k + hb) ^ i) & 7) << 4)), st.q[kHeadSteps + k], s[kb]);
+      s[kb] = mfma(*reinterpret_cast<const bf16x8*>(t.rope + 32 * kb * kRopeBytes + at.rope[k]), st.q[kHeadSteps + k], s[kb]);
   }
   float top = -INFINITY;
+  const int own_limit = limit - 4 * hb;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      s[kb][r] *= scale_log2;
-      if (masked && 32 * kb + acc_row(r, hb) >= limit) s[kb][r] = -INFINITY;
+      if (MASKED && 32 * kb + acc_row(r, 0) >= own_limit) s[kb][r] = -INFINITY;
       top = fmaxf(top, s[kb][r]);
     }
-  top = fmaxf(top, other_half(top, lane));
+  top = fmaxf(top, other_half(top, lane)) * scale_log2;
   if (__any(top > st.m + kLazy)) {
     const float m = fmaxf(st.m, top);
     const float f = __builtin_amdgcn_exp2f(st.m - m);
@@ -163,23 +237,22 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, int li
   for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const float w = __builtin_amdgcn_exp2f(s[kb][r] - st.m);
+      const float w = __builtin_amdgcn_exp2f(fmaf(s[kb][r], scale_log2, -st.m));
       st.l += w;
+      if (MASKED) s[kb][r] = w;
       p[2 * kb + (r >> 3)][r & 7] = (__bf16)w;
     }
-  const int j = lane & 15, quarter = (lane >> 4) & 1;
+  if (MASKED && values_not_finite(t, here(lane))) {
+    add_values_one_by_one(st.o, s, t, limit, here(lane));
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k)
 #pragma unroll
     for (int cb = 0; cb < kColBlocks; ++cb) {
-      const int chunk = cb * 4 + 2 * quarter + ((j & 3) >> 1);
-      bf16x4 v[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int key = 16 * k + 8 * e + 4 * hb + (j >> 2);
-        v[e] = read_tr(t.up + key * kUpBytes + kUpBytes / 2 + ((chunk ^ swizzle(key)) << 4) + (j & 1) * 8);
-      }
-      st.o[cb] = mfma(join8(v[0], v[1]), p[k], st.o[cb]);
+      // rows 8 further swizzle with bit 3 flipped: the offset of column block cb ^ 2
+      const char* v = t.up + 16 * k * kUpBytes;
+      st.o[cb] = mfma(join8(read_tr(v + at.value[cb]), read_tr(v + 8 * kUpBytes + at.value[cb ^ 2])), p[k], st.o[cb]);
     }
 }
 
@@ -218,22 +291,43 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
 #pragma unroll
   for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x16{};
   {
+    // a negative scale goes into the signs of q: the largest product is then the largest score
+    const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     const uint16_t* q = a.q + (blk.q0 + row) * a.q_token_stride + head * a.q_head_stride + hb * 8;
 #pragma unroll
     for (int k = 0; k < kHeadSteps + kRopeSteps; ++k) {
-      st.q[k] = bf16x8{};
-      if (live) st.q[k] = *reinterpret_cast<const bf16x8*>(q + k * 16);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (live) v = *reinterpret_cast<const uint4*>(q + k * 16);
+      st.q[k] = __builtin_bit_cast(bf16x8, make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign));
     }
   }
+  const float scale_log2 = fabsf(a.scale_log2);
 
-  if (wg_keys > 0) load_tile(a, blk, head, 0, stage0, lane, wave);
+  const TileReads reads = tile_reads(lane);
+  const TileLoads loads = tile_loads(a, kKeys, lane, wave);
+  const char* up = reinterpret_cast<const char*>(a.kv + blk.k0 * a.kv_token_stride + head * a.kv_head_stride);
+  const char* rope = reinterpret_cast<const char*>(a.rope + blk.k0 * a.rope_stride);
+  // tiles may reach past the workgroup's keys, but not past the request's
+  auto queue = [&](int64_t j0, Stage& st_to) {
+    const char* u = up + j0 * a.kv_token_stride * 2;
+    const char* r = rope + j0 * a.rope_stride * 2;
+    const int64_t rows = blk.nk - j0;
+    TileLoads t = loads;
+    if (rows < kKeys) t = tile_loads(a, (int)rows, here(lane), wave);
+    load_tile(u, r, t, st_to, wave);
+  };
+  if (wg_keys > 0) queue(0, stage0);
   auto step = [&](int64_t j0, const Stage& cur, Stage& nxt) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier();              // every wave's rows are there, and nobody reads the other stage any more
-    if (j0 + kKeys < wg_keys) load_tile(a, blk, head, j0 + kKeys, nxt, lane, wave);
+    if (j0 + kKeys < wg_keys) queue(j0 + kKeys, nxt);
     if (j0 >= wave_most) return;
-    const int64_t left = own_keys - j0;
-    attend_tile(st, cur, (int)(left < 0 ? 0 : (left < kKeys ? left : kKeys)), j0 + kKeys > wave_least, a.scale_log2, lane);
+    if (j0 + kKeys <= wave_least) {
+      attend_tile<false>(st, cur, reads, kKeys, scale_log2, lane);
+    } else {
+      const int64_t left = own_keys - j0;
+      attend_tile<true>(st, cur, reads, (int)(left < 0 ? 0 : (left < kKeys ? left : kKeys)), scale_log2, lane);
+    }
   };
   for (int64_t j0 = 0; j0 < wg_keys; j0 += 2 * kKeys) {
     step(j0, stage0, stage1);

@@ -433,6 +433,32 @@ def test_expanded(lib, dev, name):
                     assert err is None, err
 
 
+def test_expanded_not_finite_where_masked(lib, dev):
+    """Keys and values that hold NaN or an infinity reach the queries that
+    attend them and no other, also those of the same tile."""
+    import torch
+    rng = np.random.default_rng(60)
+    n, H = 200, 2
+    q, qh = _bf(rng, (n, H, 192), dev)
+    kv, kvh = _bf(rng, (n, H, 256), dev)
+    rope, rh = _bf(rng, (n, 64), dev)
+    kv[100, 0, 130] = float("inf")          # head 0: a value column
+    kv[150, 0, 3] = float("nan")            # head 0: a key
+    rope[180, 5] = float("nan")             # every head's key
+    out, lse = lib.latent_attention_expanded(q, kv, rope, _i32([0, n], dev), _i32([0, n], dev), 0.1)
+    out, lse = _host(out), _host(lse)
+    assert np.isfinite(lse[:150]).all() and np.isfinite(out[:100]).all() and np.isfinite(out[:180, 1]).all()
+    assert np.isposinf(out[100:150, 0, 2]).all() and np.isfinite(np.delete(out[:150, 0], 2, axis=1)).all()
+    assert np.isnan(out[150:, 0]).all() and np.isnan(out[180:, 1]).all() and np.isfinite(lse[:180, 1]).all()
+    for i in (0, 63, 64, 99, 149):
+        for h in range(H):
+            v = kvh[:i + 1, h, 128:].copy()
+            a = lo.attend(qh[i, h], np.concatenate([kvh[:i + 1, h, :128], rh[:i + 1]], 1), v, 0.1)
+            keep = np.arange(128) != 2 if (h == 0 and i >= 100) else np.ones(128, bool)
+            assert lo.check("out", out[i, h][keep], a.out[keep], a.out_bound[keep]) is None
+            assert lo.check("lse", lse[i, h], a.lse, a.lse_bound) is None
+
+
 # ---- together, captured, on other streams ------------------------------------------------------------------
 
 def _forms_agree(lib, dev, stream=None):
