@@ -49,25 +49,22 @@ constexpr int kTileRope = kTileKeys * kRopeBytes;
 
 __device__ __attribute__((aligned(16))) const char kZeroRow[kRowBytes] = {};
 
-// A workgroup's LDS: a ring of stages (one tile's rows as they are loaded),
-// for E4M3 the current tile's rows as bf16 and the keys' scales, and the
-// waves' parts of the scores (E4M3 of up to two pairs: in the codes that have
-// been widened).  Sized so that two workgroups share a CU where they can, each
-// with one tile on its way while one is computed; where only one fits, two
-// tiles are on their way.
+// A workgroup's LDS: a ring of stages (one tile's rows as they are loaded), the
+// keys' scales (E4M3), the tiles' list entries, and the waves' parts of the
+// scores.  Sized so that two workgroups share a CU where they can; bf16 rows of
+// one pair then have one tile on its way while one is computed, all others two.
 template <int PAIRS, bool E4M3>
 struct Lds {
   static constexpr int kWaves = 2 * PAIRS;
   static constexpr int kLatentBytes = E4M3 ? kTileCodes : kTileLatent;
   static constexpr int kStageBytes = kLatentBytes + kTileRope;
-  static constexpr int kAhead = PAIRS == 1 || (PAIRS == 2 && E4M3) ? 1 : 2;   // tiles on their way
+  static constexpr int kAhead = PAIRS == 1 && !E4M3 ? 1 : 2;                  // tiles on their way
   static constexpr int kStages = kAhead + 1;
-  static constexpr bool kSwapInCodes = E4M3 && PAIRS <= 2;
-  static constexpr int kWide = kStages * kStageBytes;
-  static constexpr int kScales = kWide + (E4M3 ? kTileLatent : 0);            // a wave's own: 64 a stage
-  static constexpr int kEntries = kScales + (E4M3 ? kWaves * kStages * 256 : 0);   // a wave's own: two tiles
-  static constexpr int kSwap = kEntries + (kAhead > 1 ? kWaves * 2 * 256 : 0);
-  static constexpr int kBytes = kSwap + (kSwapInCodes ? 0 : kWaves * 4096);
+  static constexpr int kScales = kStages * kStageBytes;                       // a wave's own: 32 a stage
+  static constexpr int kEntries = kScales + (E4M3 ? kWaves * kStages * 128 : 0);   // a wave's own: two tiles
+  static constexpr int kSwap = kEntries + (kAhead > 1 ? kWaves * 2 * 128 : 0);
+  static constexpr int kBytes = kSwap + kWaves * 4096;
+  static_assert(!E4M3 || kAhead > 1, "scales are loaded into LDS");
   // loads of rows a wave queues per tile, at least
   static constexpr int kLoads = (E4M3 ? kTileKeys / 2 : kTileKeys) / kWaves + (kWaves <= 4 ? 4 / kWaves : 0);
 };
@@ -125,6 +122,13 @@ __device__ __forceinline__ int64_t selected_tiles(const AttendArgs& a, const Tok
   return 0;
 }
 
+// The same as swizzle() for rows of codes: 8-byte reads of one chunk of 16
+// consecutive rows, and transposed reads whose 16 lanes cover one chunk of rows
+// 0..3 and 8..11 (or 4..7 and 12..15) after a multiple of 16.
+__device__ __forceinline__ int code_swizzle(int row) {
+  return (row & 3) | ((row >> 1) & 4) | ((row << 1) & 8);
+}
+
 // A slot's row; zeros for a slot below 0.  (Selected, not branched on: a tile
 // takes 32 of them.)
 __device__ __forceinline__ const char* row_at(const char* base, int64_t stride, int slot) {
@@ -144,7 +148,8 @@ __device__ __forceinline__ void load_tile(const Cache& c, int slots, uint32_t ld
       const int s0 = __builtin_amdgcn_readlane(slots, 2 * pair), s1 = __builtin_amdgcn_readlane(slots, 2 * pair + 1);
       const char* r0 = row_at(c.latent, c.latent_stride, s0);
       const char* r1 = row_at(c.latent, c.latent_stride, s1);
-      queue_to_lds((lane < 32 ? r0 : r1) + (lane & 31) * 16, lds + pair * 2 * kLatent);
+      const int sw = lane < 32 ? code_swizzle(2 * pair) : code_swizzle(2 * pair + 1);
+      queue_to_lds((lane < 32 ? r0 : r1) + ((lane & 31) ^ sw) * 16, lds + pair * 2 * kLatent);
     }
   } else {
     constexpr int kEach = kTileKeys / NW;
@@ -162,55 +167,37 @@ __device__ __forceinline__ void load_tile(const Cache& c, int slots, uint32_t ld
 #pragma unroll
   for (int i = 0; i < kRopeEach; ++i) {
     const int group = wave * kRopeEach + i;
-    const int s = __shfl(slots, group * 8 + (lane >> 3));
+    const int s = __builtin_amdgcn_ds_bpermute((group * 8 + (lane >> 3)) * 4, slots);
     const char* row = row_at(c.rope, c.rope_stride, s);
     queue_to_lds(row + ((lane ^ (lane >> 3)) & 7) * 16, lds + group * 8 * kRopeBytes);
   }
 }
 
-// E4M3 rows of a stage as bf16 rows (exact), in the layout bf16 rows are loaded in.
-template <int NW>
-__device__ __forceinline__ void widen_tile(const char* codes, char* lat, int wave) {
-  const int tid = wave * 64 + lane_here();
-#pragma unroll
-  for (int i = 0; i < kTileCodes / 16 / (64 * NW); ++i) {
-    const int at = i * 64 * NW + tid;
-    const int key = at >> 5, c = (at & 31) * 2, sw = swizzle(key);
-    const uint4 v = *reinterpret_cast<const uint4*>(codes + at * 16);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bf16x8 o[2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k], 1.0f, false);
-      const bf16x2 r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[k], 1.0f, true);
-      o[k >> 1][(k & 1) * 4 + 0] = p[0];
-      o[k >> 1][(k & 1) * 4 + 1] = p[1];
-      o[k >> 1][(k & 1) * 4 + 2] = r[0];
-      o[k >> 1][(k & 1) * 4 + 3] = r[1];
-    }
-    *reinterpret_cast<bf16x8*>(lat + key * kRowBytes + (c ^ sw) * 16) = o[0];
-    *reinterpret_cast<bf16x8*>(lat + key * kRowBytes + ((c + 1) ^ sw) * 16) = o[1];
-  }
-}
-
 // A lane's LDS offsets within a tile, for its wave's half of the values.  The
-// other offsets differ from these in bits that the swizzle only flips: chunk
-// 2 k + hb in bits 5 to 7 (key, rope), column block cb in bits 6 and 7
-// (value).  They are formed where they are read: as registers of their own they
-// would push Q and O^T out.
+// other offsets differ from these in bits that the swizzle only flips (bf16:
+// chunk 2 k + hb in bits 5 to 7, column block in bits 6 and 7; codes: chunk k
+// in bits 4 to 7, column block in bits 5 to 7).  They are formed where they are
+// read: as registers of their own they would push Q and O^T out.
 struct TileReads {
-  int key;      // row lane % 32, 16-byte chunk hb
+  int key;      // row lane % 32, its first 8 values
   int rope;
-  int value;    // transposed reads of rows 4 hb + 0..3, column block 0
+  int value;    // transposed reads of a step's rows, column block 0
 };
 
+template <bool E4M3>
 __device__ __forceinline__ TileReads tile_reads(int half, int lane) {
   const int i = lane & 31, hb = lane >> 5, j = lane & 15, quarter = (lane >> 4) & 1;
-  const int key = 4 * hb + (j >> 2);
   TileReads t;
-  t.key = i * kRowBytes + half * (kRowBytes / 2) + ((hb ^ swizzle(i)) << 4);
   t.rope = i * kRopeBytes + ((((2 * half * kRopeSteps + hb) ^ i) & 7) << 4);
-  t.value = key * kRowBytes + half * (kRowBytes / 2) + (((2 * quarter + ((j & 3) >> 1)) ^ swizzle(key)) << 4) + (j & 1) * 8;
+  if (E4M3) {
+    const int row = (j >> 1) & 3, key = row + 4 * hb + 8 * (j >> 3);
+    t.key = i * kLatent + half * (kLatent / 2) + (code_swizzle(i) << 4) + hb * 8;
+    t.value = key * kLatent + half * (kLatent / 2) + ((quarter ^ code_swizzle(key)) << 4) + (j & 1) * 8;
+  } else {
+    const int key = 4 * hb + (j >> 2);
+    t.key = i * kRowBytes + half * (kRowBytes / 2) + ((hb ^ swizzle(i)) << 4);
+    t.value = key * kRowBytes + half * (kRowBytes / 2) + (((2 * quarter + ((j & 3) >> 1)) ^ swizzle(key)) << 4) + (j & 1) * 8;
+  }
   return t;
 }
 
@@ -222,21 +209,29 @@ __device__ __forceinline__ f32x16 score_tile(const HeadState& st, const char* la
   const int hb = lane >> 5;
   f32x16 s = {};
   const int key = here(at.key);
-  auto read = [&](int k) {
-    const char* from = k < kLatentSteps ? lat + (k >> 3) * 256 + (key ^ ((k & 7) << 5)) : rope + (at.rope ^ ((k - kLatentSteps) << 5));
-    return *reinterpret_cast<const bf16x8*>(from);
-  };
-  run_ahead<kLatentSteps + kRopeSteps, kReadsAhead>(read, [&](int k, bf16x8 rows) {
-    if (E4M3 && k == kLatentSteps) {
+  auto scale_by_keys = [&] {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * g + e] *= sc[e];
-      }
+      for (int e = 0; e < 4; ++e) s[4 * g + e] *= sc[e];
     }
-    s = mfma(rows, st.q[k], s);
-  });
+  };
+  if constexpr (E4M3) {
+    run_ahead<kLatentSteps, kReadsAhead>([&](int k) { return *reinterpret_cast<const uint2*>(lat + (key ^ (k << 4))); },
+                                         [&](int k, uint2 codes) { s = mfma(widen8(codes), st.q[k], s); });
+    scale_by_keys();
+#pragma unroll
+    for (int k = 0; k < kRopeSteps; ++k)
+      s = mfma(*reinterpret_cast<const bf16x8*>(rope + (at.rope ^ (k << 5))), st.q[kLatentSteps + k], s);
+  } else {
+    run_ahead<kLatentSteps + kRopeSteps, kReadsAhead>(
+        [&](int k) {
+          return *reinterpret_cast<const bf16x8*>(k < kLatentSteps ? lat + (k >> 3) * 256 + (key ^ ((k & 7) << 5))
+                                                                   : rope + (at.rope ^ ((k - kLatentSteps) << 5)));
+        },
+        [&](int k, bf16x8 rows) { s = mfma(rows, st.q[k], s); });
+  }
   return s;
 }
 
@@ -281,14 +276,21 @@ __device__ __forceinline__ void weigh_tile(HeadState& st, f32x16 s, const char* 
     }
   }
   const int value = here(at.value);
-  run_ahead<2 * kColBlocks, kReadsAhead>(
-      [&](int i) {
-        // rows 8 further swizzle with bit 3 flipped: the offset of column block cb ^ 2
-        const int k = i / kColBlocks, cb = i % kColBlocks;
-        const char* v = lat + 16 * k * kRowBytes + (cb >> 2) * 256;
-        return join8(read_tr(v + (value ^ ((cb & 3) << 6))), read_tr(v + 8 * kRowBytes + (value ^ (((cb & 3) ^ 2) << 6))));
-      },
-      [&](int i, bf16x8 cols) { st.o[i % kColBlocks] = mfma(cols, p[i / kColBlocks], st.o[i % kColBlocks]); });
+  auto use = [&](int i, bf16x8 cols) { st.o[i % kColBlocks] = mfma(cols, p[i / kColBlocks], st.o[i % kColBlocks]); };
+  if constexpr (E4M3) {
+    run_ahead<2 * kColBlocks, kReadsAhead>(
+        [&](int i) { return read_tr8(lat + 16 * (i / kColBlocks) * kLatent + (value ^ ((i % kColBlocks) << 5))); },
+        [&](int i, uint2 codes) { use(i, widen8(codes)); });
+  } else {
+    run_ahead<2 * kColBlocks, kReadsAhead>(
+        [&](int i) {
+          // rows 8 further swizzle with bit 3 flipped: the offset of column block cb ^ 2
+          const int k = i / kColBlocks, cb = i % kColBlocks;
+          const char* v = lat + 16 * k * kRowBytes + (cb >> 2) * 256;
+          return join8(read_tr(v + (value ^ ((cb & 3) << 6))), read_tr(v + 8 * kRowBytes + (value ^ (((cb & 3) ^ 2) << 6))));
+        },
+        use);
+  }
 }
 
 // Last of the n ascending starts at or below v, 64 at a time; wave-uniform.
@@ -423,7 +425,7 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
     if (PAGED) b = count_starts(a.q_starts, a.num_requests, t, lane);
   }
 
-  const TileReads reads = tile_reads(half, lane);
+  const TileReads reads = tile_reads<E4M3>(half, lane);
   const float scale_log2 = fabsf(a.scale_log2);
   while (lo < hi) {
     // the part [first, last) of token t's n tiles
@@ -469,29 +471,25 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
     // loop is the compiler's to wait for.
     uint32_t masks[L::kAhead + 1];
     int entry = 0;                        // kAhead == 1: of the tile to be queued next
-    float scale = 0.f;                    // and lane i: the scale of key i of the tile queued last
     int into = 0;                         // the stage of the tile to be queued next
-    char* own_entries = lds + L::kEntries + wave * 512;
-    float* scales = reinterpret_cast<float*>(lds + L::kScales + wave * L::kStages * 256);
+    const char* own_entries = lds + L::kEntries + wave * 256;
+    const float* scales = reinterpret_cast<const float*>(lds + L::kScales + wave * L::kStages * 128);
     lds_barrier();                        // the last part's reads are done
     auto load_entries = [&](int64_t tile) {
       const int32_t* at = entry_of<PAGED>(a, tk, tile);
       if (L::kAhead > 1)
-        queue_word_to_lds(at, lds_base + L::kEntries + wave * 512 + (uint32_t)(tile & 1) * 256);
+        queue_words_to_lds(at, lds_base + L::kEntries + wave * 256 + (uint32_t)(tile & 1) * 128);
       else
         entry = *at;
     };
     auto queue = [&](int64_t tile, uint32_t& mask) {
-      if (L::kAhead > 1) entry = *reinterpret_cast<const int*>(own_entries + (tile & 1) * 256 + lane_here() * 4);
+      if (L::kAhead > 1) entry = *reinterpret_cast<const int*>(own_entries + (tile & 1) * 128 + (lane_here() & 31) * 4);
       const int slot = slot_of<PAGED>(a, tk, entry, tile);
       mask = (uint32_t)__ballot(slot >= 0);
       if (tile + 1 < end) load_entries(tile + 1);
       if (E4M3) {
         const float* at = slot >= 0 ? a.cache.scale + slot : reinterpret_cast<const float*>(kZeroRow);
-        if (L::kAhead > 1)
-          queue_word_to_lds(at, lds_base + L::kScales + (wave * L::kStages + into) * 256);
-        else
-          scale = *at;
+        queue_words_to_lds(at, lds_base + L::kScales + (wave * L::kStages + into) * 128);
       }
       load_tile<NW, E4M3>(a.cache, slot, lds_base + into * L::kStageBytes, wave);
       into = into + 1 < L::kStages ? into + 1 : 0;
@@ -514,7 +512,6 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
         wait_loads<L::kLoads>();          // all but the next tile's rows
       else
         wait_loads<0>();
-      if (E4M3 && L::kAhead == 1) scales[from * 64 + lane_here()] = scale;
       lds_barrier();            // every wave's rows are there, and nobody reads the stage before any more
       masks[L::kAhead] = 0;
       if (tile + L::kAhead < end) queue(tile + L::kAhead, masks[L::kAhead]);
@@ -522,27 +519,23 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
 #pragma unroll
       for (int d = 0; d < L::kAhead; ++d) masks[d] = masks[d + 1];
       char* stage = lds + from * L::kStageBytes;
-      const float* sc = scales + from * 64;
+      const float* sc = scales + from * 32;
       from = from + 1 < L::kStages ? from + 1 : 0;
-      const char* lat = stage;
-      if (E4M3) {
-        widen_tile<NW>(stage, lds + L::kWide, wave);
-        lat = lds + L::kWide;
-        lds_barrier();
-      }
-      float* swap = reinterpret_cast<float*>(L::kSwapInCodes ? stage : lds + L::kSwap) + lane * 4;
-      f32x16 s = score_tile<E4M3>(st, lat, stage + L::kLatentBytes, sc, reads, lane);
+      float* swap = reinterpret_cast<float*>(lds + L::kSwap) + lane_here() * 4;
+      f32x16 s = score_tile<E4M3>(st, stage, stage + L::kLatentBytes, sc, reads, lane);
 #pragma unroll
       for (int g = 0; g < 4; ++g)
         *reinterpret_cast<f32x4*>(swap + wave * 1024 + g * 256) = f32x4{s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]};
       lds_barrier();
+      f32x4 o[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 o = *reinterpret_cast<const f32x4*>(swap + (wave ^ 1) * 1024 + g * 256);
+      for (int g = 0; g < 4; ++g) o[g] = *reinterpret_cast<const f32x4*>(swap + (wave ^ 1) * 1024 + g * 256);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * g + e] += o[e];
-      }
-      weigh_tile<E4M3>(st, s, lat, sc, mask, scale_log2, reads, lane);
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[4 * g + e] += o[g][e];
+      weigh_tile<E4M3>(st, s, stage, sc, mask, scale_log2, reads, lane);
     }
 
     // this lane's head: its sum is spread over the two half-waves
@@ -599,12 +592,33 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
 }
 
 // Joins the parts of a token: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.
-// A workgroup takes 32 heads and one block of 32 latent values, a wave 8 of
-// these: elements stay in the accumulators' order, so reads are contiguous.
+// A workgroup takes 32 heads and one block of 32 latent values; its waves take
+// every fourth part each, with a running reference as in the main kernel and
+// kJoinAhead parts' loads in flight, and are then joined through LDS.  Elements
+// stay in the accumulators' order, so reads are contiguous.  (With one part at
+// a time a token in 64 parts took 22 us, all latency.)
+constexpr int kJoinWaves = 4;
+constexpr int kJoinAhead = 4;
+
+struct JoinState {
+  f32x4 o[4];
+  float m, l;
+  __device__ __forceinline__ void add(float pm, float pl, const f32x4 (&po)[4]) {
+    const float to = fmaxf(m, pm);
+    const float f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(pm - to);
+    m = to;
+    l = l * f + pl * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = o[i] * f + po[i] * g;
+  }
+};
+
 template <int PAIRS>
-__global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttendArgs a) {
   constexpr int NW = 2 * PAIRS;
-  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  __shared__ f32x4 others_o[kJoinWaves - 1][4][64];
+  __shared__ float2 others_ml[kJoinWaves - 1][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t t = blockIdx.x;
   const int heads = blockIdx.y, half = blockIdx.z / kColBlocks, cb = blockIdx.z % kColBlocks;
   if (!a.indices && t >= (int64_t)a.q_starts[a.num_requests]) return;
@@ -614,28 +628,54 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
   const int wave = 2 * (heads % PAIRS) + half;
   const int i = lane & 31, hb = lane >> 5;
   auto place = [&](int p) { return (base + (p == 0 ? a.wgs + g0 : g0 + p)) * NW + wave; };
-  float m = kNoMax;
-  for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[place(p) * 32 + i].x);
-  float l = 0.f;
-  f32x4 o = {};
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float2 ml = a.part_ml[place(p) * 32 + i];
-    const f32x4 v = *reinterpret_cast<const f32x4*>(a.part_out + place(p) * (16 * kLatent) + (cb * 4 + g) * 256 + lane * 4);
-    const float f = __builtin_amdgcn_exp2f(ml.x - m);
-    l = fmaf(f, ml.y, l);
+  JoinState st;
+  st.m = kNoMax;
+  st.l = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = fmaf(f, v[e], o[e]);
+  for (int g = 0; g < 4; ++g) st.o[g] = f32x4{};
+  for (int p0 = w; p0 < parts; p0 += kJoinWaves * kJoinAhead) {
+    float2 ml[kJoinAhead];
+    f32x4 o[kJoinAhead][4];
+#pragma unroll
+    for (int d = 0; d < kJoinAhead; ++d) {
+      const int p = p0 + d * kJoinWaves;
+      const int64_t at = place(p < parts ? p : p0);
+      ml[d] = a.part_ml[at * 32 + i];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        o[d][g] = *reinterpret_cast<const f32x4*>(a.part_out + at * (16 * kLatent) + (cb * 4 + g) * 256 + lane * 4);
+    }
+#pragma unroll
+    for (int d = 0; d < kJoinAhead; ++d)
+      if (p0 + d * kJoinWaves < parts) st.add(ml[d].x, ml[d].y, o[d]);
+  }
+  if (w > 0) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) others_o[w - 1][g][lane] = st.o[g];
+    others_ml[w - 1][lane] = make_float2(st.m, st.l);
+  }
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int other = 0; other < kJoinWaves - 1; ++other) {
+    const float2 ml = others_ml[other][lane];
+    f32x4 o[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) o[g] = others_o[other][g][lane];
+    st.add(ml.x, ml.y, o);
   }
   const int head = heads * 32 + i;
   if (head >= a.num_heads) return;
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = st.l > 0.f ? 1.0f / st.l : 0.f;
   const int64_t row = t * a.num_heads + head;
-  bf16x4 v;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = (__bf16)(o[e] * inv);
-  *reinterpret_cast<bf16x4*>(a.out + row * kLatent + half * (kLatent / 2) + cb * 32 + 8 * g + 4 * hb) = v;
-  if (a.lse && blockIdx.z == 0 && g == 0 && hb == 0) a.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+  for (int g = 0; g < 4; ++g) {
+    bf16x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (__bf16)(st.o[g][e] * inv);
+    *reinterpret_cast<bf16x4*>(a.out + row * kLatent + half * (kLatent / 2) + cb * 32 + 8 * g + 4 * hb) = v;
+  }
+  if (a.lse && blockIdx.z == 0 && hb == 0) a.lse[row] = st.l > 0.f ? (st.m + __log2f(st.l)) * kLn2 : -INFINITY;
 }
 
 int head_blocks(int num_heads, int pairs) { return (num_heads + 32 * pairs - 1) / (32 * pairs); }
@@ -653,13 +693,23 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream) {
   e = hipGetLastError();
   if (e != hipSuccess || a.wgs == 0) return e;
   hipLaunchKernelGGL(join_kernel<PAIRS>, dim3((unsigned)a.num_tokens, (unsigned)((a.num_heads + 31) / 32), 2 * kColBlocks),
-                     dim3(256), 0, stream, a);
+                     dim3(64 * kJoinWaves), 0, stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int attend_pairs(int num_heads) { return num_heads <= 32 ? 1 : (num_heads <= 64 ? 2 : 4); }
+
+int attend_per_cu(int num_heads, bool e4m3) {
+  int lds = 0;
+  switch (attend_pairs(num_heads)) {
+    case 1: lds = e4m3 ? Lds<1, true>::kBytes : Lds<1, false>::kBytes; break;
+    case 2: lds = e4m3 ? Lds<2, true>::kBytes : Lds<2, false>::kBytes; break;
+    default: lds = e4m3 ? Lds<4, true>::kBytes : Lds<4, false>::kBytes; break;
+  }
+  return 2 * lds <= 160 * 1024 ? 2 : 1;
+}
 
 SplitLayout split_layout(int num_tokens, int num_heads, int wgs) {
   const int pairs = attend_pairs(num_heads);

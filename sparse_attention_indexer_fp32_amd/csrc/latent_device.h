@@ -43,8 +43,33 @@ __device__ __forceinline__ bf16x4 read_tr(const char* lds) {
   return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)lds));
 }
 
+// The same for 8-bit elements: lane j names 8 bytes (columns 8 (j % 2) .. + 7) of
+// row j / 2 of 8, and gets column j of the 8 rows.
+__device__ __forceinline__ uint2 read_tr8(const char* lds) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) i32x2* lds_ptr;
+  const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)lds);
+  return make_uint2((uint32_t)v[0], (uint32_t)v[1]);
+}
+
+// Eight E4M3 codes as bf16, exactly.
+__device__ __forceinline__ bf16x8 widen8(uint2 codes) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes.x, 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes.x, 1.0f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes.y, 1.0f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes.y, 1.0f, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 __device__ __forceinline__ bf16x8 join8(bf16x4 lo, bf16x4 hi) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The lane's number, worked out where it is used (nothing is kept in a register for it).
+__device__ __forceinline__ int lane_here() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
 }
 
 // 16 bytes per lane from src (a per-lane address) into LDS at dst + 16 * lane
@@ -68,9 +93,10 @@ __device__ __forceinline__ void queue_to_lds(const char* src, uint32_t lds) {
                :: "v"(src), "s"(lds) : "m0", "memory");
 }
 
-// 4 bytes per lane, to lds + 4 * lane.
-__device__ __forceinline__ void queue_word_to_lds(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+// 4 bytes per lane of the lower half-wave, to lds + 4 * lane.
+__device__ __forceinline__ void queue_words_to_lds(const void* src, uint32_t lds) {
+  if (lane_here() < 32)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                :: "v"(src), "s"(lds) : "m0", "memory");
 }
 
@@ -118,13 +144,6 @@ __device__ __forceinline__ float other_half(float v, int lane) {
 __device__ __forceinline__ int here(int v) {
   asm volatile("" : "+v"(v));
   return v;
-}
-
-// The lane's number, worked out where it is used (nothing is kept in a register for it).
-__device__ __forceinline__ int lane_here() {
-  int l;
-  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
-  return l;
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;

@@ -111,6 +111,7 @@ struct AttendArgs {
 
 // Pairs of waves of a workgroup (32 heads each) by head count, and workspace of a split launch.
 int attend_pairs(int num_heads);
+int attend_per_cu(int num_heads, bool e4m3);   // workgroups a CU holds
 struct SplitLayout {
   size_t out_bytes, ml_bytes, rec_bytes;
   size_t total() const { return out_bytes + ml_bytes + rec_bytes; }
