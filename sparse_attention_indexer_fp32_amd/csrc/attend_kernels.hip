@@ -7,21 +7,24 @@
 //
 // One pass over the rows with a running reference maximum and sum per head.
 //
-// Tiling.  A pair of waves owns 32 heads, a workgroup 1, 2 or 4 pairs (up to
-// 128 heads); a tile is 32 keys.  Both products are taken transposed,
-//   S^T = K Q^T   (rows: keys,          columns: heads),
-//   O^T = V^T P^T (rows: latent values, columns: heads),
+// Tiling.  A wave owns 16 heads, a workgroup 1, 2, 4 or 8 waves (up to 128
+// heads); a tile is 32 keys.  Both products are taken transposed,
+//   S^T = K Q^T   (rows: keys,          columns: heads; 18 steps of 32 values),
+//   O^T = V^T P^T (rows: latent values, columns: heads; one step of 32 keys),
 // so that a lane keeps one head throughout: its column of S^T, that head's
-// maximum and sum, and its column of O^T.  A lane's 16 scores of a tile are then
+// maximum and sum, and its column of O^T.  A lane's 8 scores of a tile are then
 // exactly the elements of P^T that it has to feed to the second product, when
-// the keys of a step are taken in the order the accumulator holds them:
-// weights never leave their registers.  The pair splits a row of the cache:
-// each wave multiplies out half of the 576 values for S^T (the halves are
-// added through LDS, and both waves then hold the same weights) and makes half
-// of O^T's 512 rows.  Its Q (18 x 4 registers) and O^T (8 x 16) stay in
-// registers for all keys, two waves to a SIMD.  (One wave for 32 whole heads needs 144 +
-// 256 registers and spills.)  K is read from LDS 16 bytes a lane, V by
-// transposed reads of the same bytes.
+// the keys of that step are taken in the order the accumulators hold them:
+// weights never leave their registers, and the waves of a workgroup share
+// nothing but the rows.  Q (18 x 4 registers) and O^T (32 x 4) stay in
+// registers for all keys, two waves to a SIMD.  K is read from LDS 16 bytes a
+// lane, V by transposed reads of the same bytes; E4M3 rows stay codes in LDS
+// and are widened as they are read.
+//
+// (Waves of 32 heads would halve the LDS reads, but need 144 + 256 registers for
+// a whole row.  A pair of waves that share 32 heads by halves of the row has to
+// add its scores through LDS, with a second barrier a tile, and to repeat the
+// softmax step: 1024 tokens x 128 heads x 2048 slots took 748 us that way.)
 //
 // Rows of a tile come from anywhere in the cache, one kilobyte-long row a
 // load instruction (bf16), straight into LDS, while the previous tile is computed.  Rows
@@ -37,11 +40,12 @@
 namespace latent {
 namespace {
 
-constexpr int kLatentSteps = kLatent / 32;   // a wave's 16 steps of the first product
+constexpr int kHeads = 16;                   // heads of a wave
+constexpr int kLatentSteps = kLatent / 32;   // 16 steps of the first product
 constexpr int kRopeSteps = kRope / 32;       // and 2 of the rotary part
-constexpr int kColBlocks = kLatent / 64;     // its 8 blocks of O^T
-constexpr int kReadsAhead = 3;               // matrix instructions whose LDS reads are in flight
-constexpr int kRowBytes = kLatent * 2;       // a row as bf16 in LDS
+constexpr int kColBlocks = kLatent / 16;     // 32 blocks of O^T
+constexpr int kReadsAhead = 4;               // LDS reads in flight before a matrix instruction
+constexpr int kRowBytes = kLatent * 2;       // a bf16 row in LDS
 constexpr int kRopeBytes = kRope * 2;
 constexpr int kTileLatent = kTileKeys * kRowBytes;
 constexpr int kTileCodes = kTileKeys * kLatent;
@@ -50,29 +54,27 @@ constexpr int kTileRope = kTileKeys * kRopeBytes;
 __device__ __attribute__((aligned(16))) const char kZeroRow[kRowBytes] = {};
 
 // A workgroup's LDS: a ring of stages (one tile's rows as they are loaded), the
-// keys' scales (E4M3), the tiles' list entries, and the waves' parts of the
-// scores.  Sized so that two workgroups share a CU where they can; bf16 rows of
-// one pair then have one tile on its way while one is computed, all others two.
-template <int PAIRS, bool E4M3>
+// keys' scales (E4M3) and the tiles' list entries.  Two workgroups of up to 64
+// heads share a CU, with one bf16 tile or two of codes on their way while one is
+// computed; 128 heads take all of a CU's registers.
+template <int NW, bool E4M3>
 struct Lds {
-  static constexpr int kWaves = 2 * PAIRS;
   static constexpr int kLatentBytes = E4M3 ? kTileCodes : kTileLatent;
   static constexpr int kStageBytes = kLatentBytes + kTileRope;
-  static constexpr int kAhead = PAIRS == 1 && !E4M3 ? 1 : 2;                  // tiles on their way
+  static constexpr int kAhead = NW < 8 && !E4M3 ? 1 : 2;                      // tiles on their way
   static constexpr int kStages = kAhead + 1;
   static constexpr int kScales = kStages * kStageBytes;                       // a wave's own: 32 a stage
-  static constexpr int kEntries = kScales + (E4M3 ? kWaves * kStages * 128 : 0);   // a wave's own: two tiles
-  static constexpr int kSwap = kEntries + (kAhead > 1 ? kWaves * 2 * 128 : 0);
-  static constexpr int kBytes = kSwap + kWaves * 4096;
+  static constexpr int kEntries = kScales + (E4M3 ? NW * kStages * 128 : 0);  // a wave's own: two tiles
+  static constexpr int kBytes = kEntries + (kAhead > 1 ? NW * 2 * 128 : 0);
   static_assert(!E4M3 || kAhead > 1, "scales are loaded into LDS");
   // loads of rows a wave queues per tile, at least
-  static constexpr int kLoads = (E4M3 ? kTileKeys / 2 : kTileKeys) / kWaves + (kWaves <= 4 ? 4 / kWaves : 0);
+  static constexpr int kLoads = (E4M3 ? kTileKeys / 2 : kTileKeys) / NW + (NW <= 4 ? 4 / NW : 0);
 };
 
-// What a wave keeps of its 32 heads and its half of the values along a row of keys.
+// What a wave keeps of its 16 heads along a row of keys.
 struct HeadState {
   bf16x8 q[kLatentSteps + kRopeSteps];
-  f32x16 o[kColBlocks];
+  f32x4 o[kColBlocks];
   float m;      // reference maximum (log2 units)
   float l;      // this lane's part of the sum
 };
@@ -124,9 +126,9 @@ __device__ __forceinline__ int64_t selected_tiles(const AttendArgs& a, const Tok
 
 // The same as swizzle() for rows of codes: 8-byte reads of one chunk of 16
 // consecutive rows, and transposed reads whose 16 lanes cover one chunk of rows
-// 0..3 and 8..11 (or 4..7 and 12..15) after a multiple of 16.
+// 4 g + 0..3 and 16 + 4 g + 0..3.
 __device__ __forceinline__ int code_swizzle(int row) {
-  return (row & 3) | ((row >> 1) & 4) | ((row << 1) & 8);
+  return (row & 3) | ((row ^ (row >> 2)) & 4) | (row & 8);
 }
 
 // A slot's row; zeros for a slot below 0.  (Selected, not branched on: a tile
@@ -173,123 +175,121 @@ __device__ __forceinline__ void load_tile(const Cache& c, int slots, uint32_t ld
   }
 }
 
-// A lane's LDS offsets within a tile, for its wave's half of the values.  The
-// other offsets differ from these in bits that the swizzle only flips (bf16:
-// chunk 2 k + hb in bits 5 to 7, column block in bits 6 and 7; codes: chunk k
-// in bits 4 to 7, column block in bits 5 to 7).  They are formed where they are
-// read: as registers of their own they would push Q and O^T out.
+// A lane's LDS offsets within a tile.  The other offsets differ from these in
+// bits that the swizzle only flips (bf16: a step's chunks in bits 6 and 7, a
+// column block's in bits 5 to 7; codes: bits 5 to 7, and 4 to 7).  They are
+// formed where they are read: as registers of their own they would push Q and
+// O^T out.
 struct TileReads {
-  int key;      // row lane % 32, its first 8 values
+  int key;      // row lane % 16, the first step's values
   int rope;
-  int value;    // transposed reads of a step's rows, column block 0
+  int value;    // transposed reads of the lane group's rows, column block 0
 };
 
 template <bool E4M3>
-__device__ __forceinline__ TileReads tile_reads(int half, int lane) {
-  const int i = lane & 31, hb = lane >> 5, j = lane & 15, quarter = (lane >> 4) & 1;
+__device__ __forceinline__ TileReads tile_reads(int lane) {
+  const int i = lane & 15, g = lane >> 4;
   TileReads t;
-  t.rope = i * kRopeBytes + ((((2 * half * kRopeSteps + hb) ^ i) & 7) << 4);
+  t.rope = i * kRopeBytes + (((g ^ i) & 7) << 4);
   if (E4M3) {
-    const int row = (j >> 1) & 3, key = row + 4 * hb + 8 * (j >> 3);
-    t.key = i * kLatent + half * (kLatent / 2) + (code_swizzle(i) << 4) + hb * 8;
-    t.value = key * kLatent + half * (kLatent / 2) + ((quarter ^ code_swizzle(key)) << 4) + (j & 1) * 8;
+    const int key = 4 * g + ((i >> 1) & 3) + 16 * (i >> 3);
+    t.key = i * kLatent + (((g >> 1) ^ code_swizzle(i)) << 4) + (g & 1) * 8;
+    t.value = key * kLatent + (code_swizzle(key) << 4) + (i & 1) * 8;
   } else {
-    const int key = 4 * hb + (j >> 2);
-    t.key = i * kRowBytes + half * (kRowBytes / 2) + ((hb ^ swizzle(i)) << 4);
-    t.value = key * kRowBytes + half * (kRowBytes / 2) + (((2 * quarter + ((j & 3) >> 1)) ^ swizzle(key)) << 4) + (j & 1) * 8;
+    const int key = 4 * g + (i >> 2);
+    t.key = i * kRowBytes + ((g ^ swizzle(i)) << 4);
+    t.value = key * kRowBytes + ((((i & 3) >> 1) ^ swizzle(key)) << 4) + (i & 1) * 8;
   }
   return t;
 }
 
-// A wave's part of a tile's scores: its half of the values.  scales (E4M3):
-// each key's scale.
+// Scores of a tile: s[b][r] is the lane's head's with key 16 b + 4 (lane / 16) + r.
+// scales (E4M3): each key's scale.
 template <bool E4M3>
-__device__ __forceinline__ f32x16 score_tile(const HeadState& st, const char* lat, const char* rope,
-                                             const float* scales, const TileReads& at, int lane) {
-  const int hb = lane >> 5;
-  f32x16 s = {};
+__device__ __forceinline__ void score_tile(const HeadState& st, f32x4 (&s)[2], const char* lat, const char* rope,
+                                           const float* scales, const TileReads& at, int lane) {
+  s[0] = f32x4{};
+  s[1] = f32x4{};
   const int key = here(at.key);
-  auto scale_by_keys = [&] {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[4 * g + e] *= sc[e];
-    }
-  };
   if constexpr (E4M3) {
-    run_ahead<kLatentSteps, kReadsAhead>([&](int k) { return *reinterpret_cast<const uint2*>(lat + (key ^ (k << 4))); },
-                                         [&](int k, uint2 codes) { s = mfma(widen8(codes), st.q[k], s); });
-    scale_by_keys();
-#pragma unroll
-    for (int k = 0; k < kRopeSteps; ++k)
-      s = mfma(*reinterpret_cast<const bf16x8*>(rope + (at.rope ^ (k << 5))), st.q[kLatentSteps + k], s);
-  } else {
-    run_ahead<kLatentSteps + kRopeSteps, kReadsAhead>(
-        [&](int k) {
-          return *reinterpret_cast<const bf16x8*>(k < kLatentSteps ? lat + (k >> 3) * 256 + (key ^ ((k & 7) << 5))
-                                                                   : rope + (at.rope ^ ((k - kLatentSteps) << 5)));
+    // rows 16 on swizzle with bit 2 flipped
+    run_ahead<2 * kLatentSteps, kReadsAhead>(
+        [&](int n) {
+          const int k = n >> 1, b = n & 1;
+          return *reinterpret_cast<const uint2*>(lat + 16 * b * kLatent + (k >> 3) * 256 + (key ^ ((k & 7) << 5) ^ (b << 6)));
         },
-        [&](int k, bf16x8 rows) { s = mfma(rows, st.q[k], s); });
+        [&](int n, uint2 codes) { s[n & 1] = mfma16(widen8(codes), st.q[n >> 1], s[n & 1]); });
+    const int g = lane >> 4;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) s[b] *= *reinterpret_cast<const f32x4*>(scales + 16 * b + 4 * g);
+  } else {
+    run_ahead<2 * kLatentSteps, kReadsAhead>(
+        [&](int n) {
+          const int k = n >> 1, b = n & 1;
+          return *reinterpret_cast<const bf16x8*>(lat + 16 * b * kRowBytes + (k >> 2) * 256 + (key ^ ((k & 3) << 6)));
+        },
+        [&](int n, bf16x8 rows) { s[n & 1] = mfma16(rows, st.q[n >> 1], s[n & 1]); });
   }
-  return s;
+  run_ahead<2 * kRopeSteps, 2 * kRopeSteps>(
+      [&](int n) {
+        return *reinterpret_cast<const bf16x8*>(rope + 16 * (n & 1) * kRopeBytes + (at.rope ^ ((n >> 1) << 6)));
+      },
+      [&](int n, bf16x8 rows) { s[n & 1] = mfma16(rows, st.q[kLatentSteps + (n >> 1)], s[n & 1]); });
 }
 
 // The softmax step and the second product of a tile whose scores are s.
 // mask: the tile's selected keys.
 template <bool E4M3>
-__device__ __forceinline__ void weigh_tile(HeadState& st, f32x16 s, const char* lat, const float* scales,
+__device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], const char* lat, const float* scales,
                                            uint32_t mask, float scale_log2, const TileReads& at, int lane) {
-  const int hb = lane >> 5;
+  const int g = lane >> 4;
   if (mask != 0xFFFFFFFFu) {
-    const uint32_t own = mask >> (4 * hb);
+    const uint32_t own = mask >> (4 * g);
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      if (!((own >> acc_row(r, 0)) & 1)) s[r] = -INFINITY;
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (!((own >> (16 * b + r)) & 1)) s[b][r] = -INFINITY;
   }
-  float top = s[0];
+  float top = s[0][0];
 #pragma unroll
-  for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-  top = fmaxf(top, other_half(top, lane)) * scale_log2;
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
+  top = max_of_4(top) * scale_log2;
   if (__any(top > st.m + kLazy)) {
     const float m = fmaxf(st.m, top);
     const float f = __builtin_amdgcn_exp2f(st.m - m);
     st.m = m;
     st.l *= f;
 #pragma unroll
-    for (int cb = 0; cb < kColBlocks; ++cb)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) st.o[cb][r] *= f;
+    for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] *= f;
   }
   // Weights in bf16 (the matrix cores' type): an unbiased half step of 2^-9 on
   // each, as large as the rounding of the result itself.  The sum keeps them in fp32.
-  bf16x8 p[2];
+  bf16x8 p;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    f32x4 sc = {1.f, 1.f, 1.f, 1.f};
-    if (E4M3) sc = *reinterpret_cast<const f32x4*>(scales + 8 * g + 4 * hb);
+  for (int b = 0; b < 2; ++b) {
+    f32x4 w;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float w = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], scale_log2, -st.m));
-      st.l += w;
-      p[g >> 1][(g & 1) * 4 + e] = (__bf16)(E4M3 ? w * sc[e] : w);
-    }
+    for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], scale_log2, -st.m));
+    st.l += (w[0] + w[1]) + (w[2] + w[3]);
+    if (E4M3) w *= *reinterpret_cast<const f32x4*>(scales + 16 * b + 4 * g);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) p[4 * b + r] = (__bf16)w[r];
   }
   const int value = here(at.value);
-  auto use = [&](int i, bf16x8 cols) { st.o[i % kColBlocks] = mfma(cols, p[i / kColBlocks], st.o[i % kColBlocks]); };
   if constexpr (E4M3) {
-    run_ahead<2 * kColBlocks, kReadsAhead>(
-        [&](int i) { return read_tr8(lat + 16 * (i / kColBlocks) * kLatent + (value ^ ((i % kColBlocks) << 5))); },
-        [&](int i, uint2 codes) { use(i, widen8(codes)); });
+    run_ahead<kColBlocks, kReadsAhead>(
+        [&](int cb) { return read_tr8(lat + (cb >> 4) * 256 + (value ^ ((cb & 15) << 4))); },
+        [&](int cb, uint2 codes) { st.o[cb] = mfma16(widen8(codes), p, st.o[cb]); });
   } else {
-    run_ahead<2 * kColBlocks, kReadsAhead>(
-        [&](int i) {
-          // rows 8 further swizzle with bit 3 flipped: the offset of column block cb ^ 2
-          const int k = i / kColBlocks, cb = i % kColBlocks;
-          const char* v = lat + 16 * k * kRowBytes + (cb >> 2) * 256;
-          return join8(read_tr(v + (value ^ ((cb & 3) << 6))), read_tr(v + 8 * kRowBytes + (value ^ (((cb & 3) ^ 2) << 6))));
+    run_ahead<kColBlocks, kReadsAhead>(
+        [&](int cb) {
+          const char* v = lat + (cb >> 3) * 256 + (value ^ ((cb & 7) << 5));
+          return join8(read_tr(v), read_tr(v + 16 * kRowBytes));
         },
-        use);
+        [&](int cb, bf16x8 cols) { st.o[cb] = mfma16(cols, p, st.o[cb]); });
   }
 }
 
@@ -370,18 +370,15 @@ __device__ void plan_split(const AttendArgs& a, SplitPlan& plan, int tid) {
   lds_barrier();
 }
 
-template <int PAIRS, bool E4M3, bool PAGED>
-__global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
-  constexpr int NW = 2 * PAIRS;
-  using L = Lds<PAIRS, E4M3>;
+template <int NW, bool E4M3, bool PAGED>
+__global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
+  using L = Lds<NW, E4M3>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pair = wave >> 1, half = wave & 1;
-  const int head0 = (blockIdx.y * PAIRS + pair) * 32;
-  const int head = head0 + (lane & 31), hb = lane >> 5;
-  const bool live_wave = head0 < a.num_heads;
+  const int head = (blockIdx.y * NW + wave) * kHeads + (lane & 15), group = lane >> 4;
+  const bool live_wave = (int)(blockIdx.y * NW + wave) * kHeads < a.num_heads;
   const bool split = a.wgs > 0;
 
   // this workgroup's tiles [lo, hi) of all tokens' tiles, beginning in token
@@ -425,7 +422,7 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
     if (PAGED) b = count_starts(a.q_starts, a.num_requests, t, lane);
   }
 
-  const TileReads reads = tile_reads<E4M3>(half, lane);
+  const TileReads reads = tile_reads<E4M3>(lane);
   const float scale_log2 = fabsf(a.scale_log2);
   while (lo < hi) {
     // the part [first, last) of token t's n tiles
@@ -447,17 +444,15 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
     st.m = kNoMax;
     st.l = 0.f;
 #pragma unroll
-    for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x16{};
+    for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x4{};
     {
       // a negative scale goes into the signs of q: the largest product is then the largest score
       const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-      const uint16_t* q = a.q + t * a.q_token_stride + (int64_t)head * a.q_head_stride + hb * 8;
+      const uint16_t* q = a.q + t * a.q_token_stride + (int64_t)head * a.q_head_stride + group * 8;
 #pragma unroll
       for (int k = 0; k < kLatentSteps + kRopeSteps; ++k) {
-        const int at = k < kLatentSteps ? (half * kLatentSteps + k) * 16
-                                        : kLatent + (half * kRopeSteps + k - kLatentSteps) * 16;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (head < a.num_heads) v = *reinterpret_cast<const uint4*>(q + at);
+        if (head < a.num_heads) v = *reinterpret_cast<const uint4*>(q + k * 32);
         st.q[k] = __builtin_bit_cast(bf16x8, make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign));
       }
     }
@@ -521,40 +516,26 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
       char* stage = lds + from * L::kStageBytes;
       const float* sc = scales + from * 32;
       from = from + 1 < L::kStages ? from + 1 : 0;
-      float* swap = reinterpret_cast<float*>(lds + L::kSwap) + lane_here() * 4;
-      f32x16 s = score_tile<E4M3>(st, stage, stage + L::kLatentBytes, sc, reads, lane);
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<f32x4*>(swap + wave * 1024 + g * 256) = f32x4{s[4 * g], s[4 * g + 1], s[4 * g + 2], s[4 * g + 3]};
-      lds_barrier();
-      f32x4 o[4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) o[g] = *reinterpret_cast<const f32x4*>(swap + (wave ^ 1) * 1024 + g * 256);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * g + e] += o[g][e];
+      f32x4 s[2];
+      score_tile<E4M3>(st, s, stage, stage + L::kLatentBytes, sc, reads, lane);
       weigh_tile<E4M3>(st, s, stage, sc, mask, scale_log2, reads, lane);
     }
 
-    // this lane's head: its sum is spread over the two half-waves
-    const float l = st.l + other_half(st.l, lane);
+    // this lane's head: its sum is spread over four lanes
+    const float l = sum_of_4(st.l);
     if (whole) {
       if (head < a.num_heads) {
         const float inv = l > 0.f ? 1.0f / l : 0.f;
         const int64_t row = t * a.num_heads + head;
-        uint16_t* out = a.out + row * kLatent + half * (kLatent / 2) + 4 * hb;
+        uint16_t* out = a.out + row * kLatent + 4 * group;
 #pragma unroll
-        for (int cb = 0; cb < kColBlocks; ++cb)
+        for (int cb = 0; cb < kColBlocks; ++cb) {
+          bf16x4 v;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            bf16x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (__bf16)(st.o[cb][4 * g + e] * inv);
-            *reinterpret_cast<bf16x4*>(out + cb * 32 + 8 * g) = v;
-          }
-        if (a.lse && hb == 0 && half == 0) a.lse[row] = l > 0.f ? (st.m + __log2f(l)) * kLn2 : -INFINITY;
+          for (int r = 0; r < 4; ++r) v[r] = (__bf16)(st.o[cb][r] * inv);
+          *reinterpret_cast<bf16x4*>(out + cb * 16) = v;
+        }
+        if (a.lse && group == 0) a.lse[row] = l > 0.f ? (st.m + __log2f(l)) * kLn2 : -INFINITY;
       }
       if (split && tid == 0 && blockIdx.y == 0) {
         a.part_rec[2 * t] = 0;
@@ -565,17 +546,10 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
       const int64_t slot = first == 0 ? a.wgs + blockIdx.x : blockIdx.x;
       const int64_t at = ((int64_t)blockIdx.y * 2 * a.wgs + slot) * NW + wave;
       if (live_wave) {
-        float* o = a.part_out + at * (16 * kLatent) + lane * 4;
+        float* o = a.part_out + at * (kHeads * kLatent) + lane * 4;
 #pragma unroll
-        for (int cb = 0; cb < kColBlocks; ++cb)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            f32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = st.o[cb][4 * g + e];
-            *reinterpret_cast<f32x4*>(o + (cb * 4 + g) * 256) = v;
-          }
-        if (hb == 0) a.part_ml[at * 32 + lane] = make_float2(st.m, l);   // the same in both waves of a pair
+        for (int cb = 0; cb < kColBlocks; ++cb) *reinterpret_cast<f32x4*>(o + cb * 256) = st.o[cb];
+        if (group == 0) a.part_ml[at * kHeads + lane] = make_float2(st.m, l);
       }
       if (first == 0 && tid == 0 && blockIdx.y == 0) {
         // the last of its tiles is held by the last workgroup g with total g / wgs <= that tile
@@ -592,58 +566,57 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attend_kernel(AttendArgs a) {
 }
 
 // Joins the parts of a token: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.
-// A workgroup takes 32 heads and one block of 32 latent values; its waves take
-// every fourth part each, with a running reference as in the main kernel and
-// kJoinAhead parts' loads in flight, and are then joined through LDS.  Elements
-// stay in the accumulators' order, so reads are contiguous.  (With one part at
-// a time a token in 64 parts took 22 us, all latency.)
+// A workgroup takes 16 heads and kJoinBlocks blocks of 16 latent values; its
+// waves take every fourth part each, with a running reference as in the main
+// kernel and kJoinAhead parts' loads in flight, and are then joined through
+// LDS.  Elements stay in the accumulators' order, so reads are contiguous.
+// (With one part at a time a token in 64 parts took 22 us, all latency.)
 constexpr int kJoinWaves = 4;
 constexpr int kJoinAhead = 4;
+constexpr int kJoinBlocks = 4;
 
 struct JoinState {
-  f32x4 o[4];
+  f32x4 o[kJoinBlocks];
   float m, l;
-  __device__ __forceinline__ void add(float pm, float pl, const f32x4 (&po)[4]) {
+  __device__ __forceinline__ void add(float pm, float pl, const f32x4 (&po)[kJoinBlocks]) {
     const float to = fmaxf(m, pm);
     const float f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(pm - to);
     m = to;
     l = l * f + pl * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * f + po[i] * g;
+    for (int i = 0; i < kJoinBlocks; ++i) o[i] = o[i] * f + po[i] * g;
   }
 };
 
-template <int PAIRS>
+template <int NW>
 __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttendArgs a) {
-  constexpr int NW = 2 * PAIRS;
-  __shared__ f32x4 others_o[kJoinWaves - 1][4][64];
+  __shared__ f32x4 others_o[kJoinWaves - 1][kJoinBlocks][64];
   __shared__ float2 others_ml[kJoinWaves - 1][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t t = blockIdx.x;
-  const int heads = blockIdx.y, half = blockIdx.z / kColBlocks, cb = blockIdx.z % kColBlocks;
+  const int heads = blockIdx.y, cb0 = blockIdx.z * kJoinBlocks;
   if (!a.indices && t >= (int64_t)a.q_starts[a.num_requests]) return;
   const int g0 = a.part_rec[2 * t], parts = a.part_rec[2 * t + 1];
   if (parts <= 1) return;
-  const int64_t base = (int64_t)(heads / PAIRS) * 2 * a.wgs;
-  const int wave = 2 * (heads % PAIRS) + half;
-  const int i = lane & 31, hb = lane >> 5;
-  auto place = [&](int p) { return (base + (p == 0 ? a.wgs + g0 : g0 + p)) * NW + wave; };
+  const int64_t base = (int64_t)(heads / NW) * 2 * a.wgs;
+  const int i = lane & 15, group = lane >> 4;
+  auto place = [&](int p) { return (base + (p == 0 ? a.wgs + g0 : g0 + p)) * NW + heads % NW; };
   JoinState st;
   st.m = kNoMax;
   st.l = 0.f;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) st.o[g] = f32x4{};
+  for (int c = 0; c < kJoinBlocks; ++c) st.o[c] = f32x4{};
   for (int p0 = w; p0 < parts; p0 += kJoinWaves * kJoinAhead) {
     float2 ml[kJoinAhead];
-    f32x4 o[kJoinAhead][4];
+    f32x4 o[kJoinAhead][kJoinBlocks];
 #pragma unroll
     for (int d = 0; d < kJoinAhead; ++d) {
       const int p = p0 + d * kJoinWaves;
       const int64_t at = place(p < parts ? p : p0);
-      ml[d] = a.part_ml[at * 32 + i];
+      ml[d] = a.part_ml[at * kHeads + i];
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        o[d][g] = *reinterpret_cast<const f32x4*>(a.part_out + at * (16 * kLatent) + (cb * 4 + g) * 256 + lane * 4);
+      for (int c = 0; c < kJoinBlocks; ++c)
+        o[d][c] = *reinterpret_cast<const f32x4*>(a.part_out + at * (kHeads * kLatent) + (cb0 + c) * 256 + lane * 4);
     }
 #pragma unroll
     for (int d = 0; d < kJoinAhead; ++d)
@@ -651,7 +624,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttendArgs a) {
   }
   if (w > 0) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) others_o[w - 1][g][lane] = st.o[g];
+    for (int c = 0; c < kJoinBlocks; ++c) others_o[w - 1][c][lane] = st.o[c];
     others_ml[w - 1][lane] = make_float2(st.m, st.l);
   }
   __syncthreads();
@@ -659,74 +632,77 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttendArgs a) {
 #pragma unroll
   for (int other = 0; other < kJoinWaves - 1; ++other) {
     const float2 ml = others_ml[other][lane];
-    f32x4 o[4];
+    f32x4 o[kJoinBlocks];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) o[g] = others_o[other][g][lane];
+    for (int c = 0; c < kJoinBlocks; ++c) o[c] = others_o[other][c][lane];
     st.add(ml.x, ml.y, o);
   }
-  const int head = heads * 32 + i;
+  const int head = heads * kHeads + i;
   if (head >= a.num_heads) return;
   const float inv = st.l > 0.f ? 1.0f / st.l : 0.f;
   const int64_t row = t * a.num_heads + head;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
+  for (int c = 0; c < kJoinBlocks; ++c) {
     bf16x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (__bf16)(st.o[g][e] * inv);
-    *reinterpret_cast<bf16x4*>(a.out + row * kLatent + half * (kLatent / 2) + cb * 32 + 8 * g + 4 * hb) = v;
+    for (int r = 0; r < 4; ++r) v[r] = (__bf16)(st.o[c][r] * inv);
+    *reinterpret_cast<bf16x4*>(a.out + row * kLatent + (cb0 + c) * 16 + 4 * group) = v;
   }
-  if (a.lse && blockIdx.z == 0 && hb == 0) a.lse[row] = st.l > 0.f ? (st.m + __log2f(st.l)) * kLn2 : -INFINITY;
+  if (a.lse && cb0 == 0 && group == 0) a.lse[row] = st.l > 0.f ? (st.m + __log2f(st.l)) * kLn2 : -INFINITY;
 }
 
-int head_blocks(int num_heads, int pairs) { return (num_heads + 32 * pairs - 1) / (32 * pairs); }
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-template <int PAIRS, bool E4M3>
+template <int NW, bool E4M3>
 hipError_t launch(const AttendArgs& a, hipStream_t stream) {
   const unsigned x = a.wgs > 0 ? (unsigned)a.wgs : (unsigned)(((int64_t)a.num_tokens + 7) / 8 * 8);
-  const dim3 grid(x, (unsigned)head_blocks(a.num_heads, PAIRS)), block(128 * PAIRS);
-  constexpr int kLds = Lds<PAIRS, E4M3>::kBytes;
+  const dim3 grid(x, (unsigned)ceil_div(a.num_heads, kHeads * NW)), block(64 * NW);
+  constexpr int kLds = Lds<NW, E4M3>::kBytes;
   static_assert(kLds <= 160 * 1024 && sizeof(SplitPlan) <= (size_t)kLds, "LDS of a workgroup");
-  auto* kernel = a.indices ? attend_kernel<PAIRS, E4M3, false> : attend_kernel<PAIRS, E4M3, true>;
+  auto* kernel = a.indices ? attend_kernel<NW, E4M3, false> : attend_kernel<NW, E4M3, true>;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess || a.wgs == 0) return e;
-  hipLaunchKernelGGL(join_kernel<PAIRS>, dim3((unsigned)a.num_tokens, (unsigned)((a.num_heads + 31) / 32), 2 * kColBlocks),
+  hipLaunchKernelGGL(join_kernel<NW>, dim3((unsigned)a.num_tokens, (unsigned)ceil_div(a.num_heads, kHeads), kColBlocks / kJoinBlocks),
                      dim3(64 * kJoinWaves), 0, stream, a);
   return hipGetLastError();
 }
 
-}  // namespace
-
-int attend_pairs(int num_heads) { return num_heads <= 32 ? 1 : (num_heads <= 64 ? 2 : 4); }
-
-int attend_per_cu(int num_heads, bool e4m3) {
-  int lds = 0;
-  switch (attend_pairs(num_heads)) {
-    case 1: lds = e4m3 ? Lds<1, true>::kBytes : Lds<1, false>::kBytes; break;
-    case 2: lds = e4m3 ? Lds<2, true>::kBytes : Lds<2, false>::kBytes; break;
-    default: lds = e4m3 ? Lds<4, true>::kBytes : Lds<4, false>::kBytes; break;
+template <bool E4M3>
+hipError_t launch_heads(const AttendArgs& a, hipStream_t stream) {
+  switch (attend_waves(a.num_heads)) {
+    case 1: return launch<1, E4M3>(a, stream);
+    case 2: return launch<2, E4M3>(a, stream);
+    case 4: return launch<4, E4M3>(a, stream);
+    default: return launch<8, E4M3>(a, stream);
   }
-  return 2 * lds <= 160 * 1024 ? 2 : 1;
 }
 
+}  // namespace
+
+int attend_waves(int num_heads) {
+  const int groups = ceil_div(num_heads, kHeads);
+  return groups <= 1 ? 1 : (groups <= 2 ? 2 : (groups <= 4 ? 4 : 8));
+}
+
+int attend_heads(int num_heads) { return kHeads * attend_waves(num_heads); }
+
+int attend_per_cu(int num_heads) { return attend_waves(num_heads) < 8 ? 2 : 1; }
+
 SplitLayout split_layout(int num_tokens, int num_heads, int wgs) {
-  const int pairs = attend_pairs(num_heads);
-  const size_t parts = (size_t)2 * wgs * head_blocks(num_heads, pairs) * 2 * pairs;   // of one wave
+  const int nw = attend_waves(num_heads);
+  const size_t parts = (size_t)2 * wgs * ceil_div(num_heads, kHeads * nw) * nw;   // of one wave
   SplitLayout s;
-  s.out_bytes = parts * 16 * kLatent * sizeof(float);
-  s.ml_bytes = parts * 32 * sizeof(float2);
+  s.out_bytes = parts * kHeads * kLatent * sizeof(float);
+  s.ml_bytes = parts * kHeads * sizeof(float2);
   s.rec_bytes = ((size_t)num_tokens * 2 * sizeof(int32_t) + 15) / 16 * 16;
   return s;
 }
 
 hipError_t launch_attend(const AttendArgs& a, bool e4m3, hipStream_t stream) {
-  switch (attend_pairs(a.num_heads)) {
-    case 1: return e4m3 ? launch<1, true>(a, stream) : launch<1, false>(a, stream);
-    case 2: return e4m3 ? launch<2, true>(a, stream) : launch<2, false>(a, stream);
-    default: return e4m3 ? launch<4, true>(a, stream) : launch<4, false>(a, stream);
-  }
+  return e4m3 ? launch_heads<true>(a, stream) : launch_heads<false>(a, stream);
 }
 
 }  // namespace latent

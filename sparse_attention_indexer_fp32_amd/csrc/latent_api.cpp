@@ -93,10 +93,10 @@ float scale_log2(float softmax_scale) {
 
 // Workgroups that share the tiles of a launch of absorbed attention, or 0 for one
 // workgroup per token.
-int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, int32_t num_requests, bool e4m3) {
-  const int pairs = latent::attend_pairs(num_heads);
-  const int64_t blocks = (num_heads + 32 * pairs - 1) / (32 * pairs);
-  const int64_t resident = (int64_t)cus * latent::attend_per_cu(num_heads, e4m3);
+int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, int32_t num_requests) {
+  const int heads = latent::attend_heads(num_heads);
+  const int64_t blocks = (num_heads + heads - 1) / heads;
+  const int64_t resident = (int64_t)cus * latent::attend_per_cu(num_heads);
   if (num_tokens > latent::kSplitTokens || num_requests > 65535 || num_tokens * blocks >= 4 * resident) return 0;
   int64_t wgs = resident / blocks;
   const int64_t tiles = num_tokens * ((keys + latent::kTileKeys - 1) / latent::kTileKeys + 1);
@@ -123,7 +123,7 @@ topk_status_t attend(latent::AttendArgs& a, int64_t keys, bool e4m3, void* works
   int cus = 0;
   const topk_status_t st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
-  a.wgs = split_wgs(cus, a.num_tokens, a.num_heads, keys, a.num_requests, e4m3);
+  a.wgs = split_wgs(cus, a.num_tokens, a.num_heads, keys, a.num_requests);
   if (a.wgs > 0) {
     const latent::SplitLayout s = latent::split_layout(a.num_tokens, a.num_heads, a.wgs);
     if (!workspace || workspace_bytes < s.total()) return invalid("the workspace is smaller than latent_attention_workspace says");
@@ -134,8 +134,8 @@ topk_status_t attend(latent::AttendArgs& a, int64_t keys, bool e4m3, void* works
     a.part_rec = reinterpret_cast<int32_t*>(p + s.out_bytes + s.ml_bytes);
   }
   char buf[160];
-  std::snprintf(buf, sizeof(buf), "latent-attention %s %s pairs=%d wgs=%d", a.indices ? "selected" : "paged",
-                e4m3 ? "e4m3" : "bf16", latent::attend_pairs(a.num_heads), a.wgs);
+  std::snprintf(buf, sizeof(buf), "latent-attention %s %s waves=%d wgs=%d", a.indices ? "selected" : "paged",
+                e4m3 ? "e4m3" : "bf16", latent::attend_waves(a.num_heads), a.wgs);
   return launched(latent::launch_attend(a, e4m3, stream), buf);
 }
 
@@ -283,11 +283,8 @@ topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, 
   int cus = 0;
   const topk_status_t st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
-  for (const bool e4m3 : {false, true}) {   // enough for either cache
-    const int wgs = split_wgs(cus, num_tokens, num_heads, keys, 0, e4m3);
-    const size_t need = wgs > 0 ? latent::split_layout(num_tokens, num_heads, wgs).total() : 0;
-    if (need > *bytes) *bytes = need;
-  }
+  const int wgs = split_wgs(cus, num_tokens, num_heads, keys, 0);
+  if (wgs > 0) *bytes = latent::split_layout(num_tokens, num_heads, wgs).total();
   return TOPK_SUCCESS;
 }
 

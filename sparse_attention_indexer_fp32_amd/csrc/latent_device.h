@@ -21,7 +21,14 @@ __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Row of accumulator register r (0..15) in half-wave hb.
+// 16x16x32 bf16 products summed in fp32.  Lane l = 16 g + i.  Operands: a holds
+// A[i][8 g + (0..7)], b holds B[8 g + (0..7)][i].  Accumulator register r holds
+// C[4 g + r][i].
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Row of accumulator register r (0..15) of a 32x32 product in half-wave hb.
 __device__ __forceinline__ int acc_row(int r, int hb) { return 8 * (r >> 2) + 4 * hb + (r & 3); }
 
 // LDS rows are cut in 16-byte chunks, and chunk c of a row sits at c ^
@@ -144,6 +151,23 @@ __device__ __forceinline__ float other_half(float v, int lane) {
 __device__ __forceinline__ int here(int v) {
   asm volatile("" : "+v"(v));
   return v;
+}
+
+// Maximum and sum over the four lanes that share lane % 16.  The swaps exchange
+// the odd rows of 16 lanes (the upper half-wave) of their first operand with
+// the even rows (the lower half) of their second: with both the same value, the
+// two results hold a row's own value and its partner's.
+__device__ __forceinline__ float max_of_4(float v) {
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float sum_of_4(float v) {
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;

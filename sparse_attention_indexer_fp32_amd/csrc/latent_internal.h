@@ -109,9 +109,11 @@ struct AttendArgs {
   int32_t* part_rec;
 };
 
-// Pairs of waves of a workgroup (32 heads each) by head count, and workspace of a split launch.
-int attend_pairs(int num_heads);
-int attend_per_cu(int num_heads, bool e4m3);   // workgroups a CU holds
+// By head count: waves of a workgroup, heads it takes, workgroups a CU holds;
+// and the workspace of a split launch.
+int attend_waves(int num_heads);
+int attend_heads(int num_heads);
+int attend_per_cu(int num_heads);
 struct SplitLayout {
   size_t out_bytes, ml_bytes, rec_bytes;
   size_t total() const { return out_bytes + ml_bytes + rec_bytes; }
