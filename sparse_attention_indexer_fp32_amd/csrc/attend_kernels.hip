@@ -203,22 +203,23 @@ __device__ __forceinline__ TileReads tile_reads(int lane) {
   return t;
 }
 
-// Scores of a tile: s[b][r] is the lane's head's with key 16 b + 4 (lane / 16) + r.
-// scales (E4M3): each key's scale.
+// Scores of a tile at LDS address lat: s[b][r] is the lane's head's with key
+// 16 b + 4 (lane / 16) + r.  scales (E4M3): each key's scale.  (Stages begin at
+// multiples of 256 bytes, so their address may be added before the xor.)
 template <bool E4M3>
-__device__ __forceinline__ void score_tile(const HeadState& st, f32x4 (&s)[2], const char* lat, const char* rope,
-                                           const float* scales, const TileReads& at, int lane) {
+__device__ __forceinline__ void score_tile(const HeadState& st, f32x4 (&s)[2], uint32_t lat, const float* scales,
+                                           const TileReads& at, int lane) {
   s[0] = f32x4{};
   s[1] = f32x4{};
-  const int key = here(at.key);
+  const uint32_t key = (uint32_t)here(at.key + (int)lat);
   if constexpr (E4M3) {
     // rows 16 on swizzle with bit 2 flipped
     run_ahead<2 * kLatentSteps, kReadsAhead>(
         [&](int n) {
           const int k = n >> 1, b = n & 1;
-          return *reinterpret_cast<const uint2*>(lat + 16 * b * kLatent + (k >> 3) * 256 + (key ^ ((k & 7) << 5) ^ (b << 6)));
+          return read_lds<u32x2>((key ^ (uint32_t)(((k & 7) << 5) ^ (b << 6))) + 16 * b * kLatent + (k >> 3) * 256);
         },
-        [&](int n, uint2 codes) { s[n & 1] = mfma16(widen8(codes), st.q[n >> 1], s[n & 1]); });
+        [&](int n, bf16x8 rows) { s[n & 1] = mfma16(rows, st.q[n >> 1], s[n & 1]); });
     const int g = lane >> 4;
 #pragma unroll
     for (int b = 0; b < 2; ++b) s[b] *= *reinterpret_cast<const f32x4*>(scales + 16 * b + 4 * g);
@@ -226,21 +227,20 @@ __device__ __forceinline__ void score_tile(const HeadState& st, f32x4 (&s)[2], c
     run_ahead<2 * kLatentSteps, kReadsAhead>(
         [&](int n) {
           const int k = n >> 1, b = n & 1;
-          return *reinterpret_cast<const bf16x8*>(lat + 16 * b * kRowBytes + (k >> 2) * 256 + (key ^ ((k & 3) << 6)));
+          return read_lds<bf16x8>((key ^ (uint32_t)((k & 3) << 6)) + 16 * b * kRowBytes + (k >> 2) * 256);
         },
         [&](int n, bf16x8 rows) { s[n & 1] = mfma16(rows, st.q[n >> 1], s[n & 1]); });
   }
+  const uint32_t rope = (uint32_t)at.rope + lat + (E4M3 ? kTileCodes : kTileLatent);
   run_ahead<2 * kRopeSteps, 2 * kRopeSteps>(
-      [&](int n) {
-        return *reinterpret_cast<const bf16x8*>(rope + 16 * (n & 1) * kRopeBytes + (at.rope ^ ((n >> 1) << 6)));
-      },
+      [&](int n) { return read_lds<bf16x8>((rope ^ (uint32_t)((n >> 1) << 6)) + 16 * (n & 1) * kRopeBytes); },
       [&](int n, bf16x8 rows) { s[n & 1] = mfma16(rows, st.q[kLatentSteps + (n >> 1)], s[n & 1]); });
 }
 
 // The softmax step and the second product of a tile whose scores are s.
 // mask: the tile's selected keys.
 template <bool E4M3>
-__device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], const char* lat, const float* scales,
+__device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], uint32_t lat, const float* scales,
                                            uint32_t mask, float scale_log2, const TileReads& at, int lane) {
   const int g = lane >> 4;
   if (mask != 0xFFFFFFFFu) {
@@ -278,18 +278,18 @@ __device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], const c
 #pragma unroll
     for (int r = 0; r < 4; ++r) p[4 * b + r] = (__bf16)w[r];
   }
-  const int value = here(at.value);
+  const uint32_t value = (uint32_t)here(at.value + (int)lat);
+  auto use = [&](int cb, bf16x8 cols) { st.o[cb] = mfma16(cols, p, st.o[cb]); };
   if constexpr (E4M3) {
     run_ahead<kColBlocks, kReadsAhead>(
-        [&](int cb) { return read_tr8(lat + (cb >> 4) * 256 + (value ^ ((cb & 15) << 4))); },
-        [&](int cb, uint2 codes) { st.o[cb] = mfma16(widen8(codes), p, st.o[cb]); });
+        [&](int cb) { return read_tr8((value ^ (uint32_t)((cb & 15) << 4)) + (cb >> 4) * 256); }, use);
   } else {
     run_ahead<kColBlocks, kReadsAhead>(
         [&](int cb) {
-          const char* v = lat + (cb >> 3) * 256 + (value ^ ((cb & 7) << 5));
+          const uint32_t v = (value ^ (uint32_t)((cb & 7) << 5)) + (cb >> 3) * 256;
           return join8(read_tr(v), read_tr(v + 16 * kRowBytes));
         },
-        [&](int cb, bf16x8 cols) { st.o[cb] = mfma16(cols, p, st.o[cb]); });
+        use);
   }
 }
 
@@ -513,11 +513,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
       const uint32_t mask = masks[0];
 #pragma unroll
       for (int d = 0; d < L::kAhead; ++d) masks[d] = masks[d + 1];
-      char* stage = lds + from * L::kStageBytes;
+      const uint32_t stage = lds_base + from * L::kStageBytes;
       const float* sc = scales + from * 32;
       from = from + 1 < L::kStages ? from + 1 : 0;
       f32x4 s[2];
-      score_tile<E4M3>(st, s, stage, stage + L::kLatentBytes, sc, reads, lane);
+      score_tile<E4M3>(st, s, stage, sc, reads, lane);
       weigh_tile<E4M3>(st, s, stage, sc, mask, scale_log2, reads, lane);
     }
 

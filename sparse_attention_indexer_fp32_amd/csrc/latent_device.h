@@ -11,6 +11,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -32,35 +33,43 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
 __device__ __forceinline__ int acc_row(int r, int hb) { return 8 * (r >> 2) + 4 * hb + (r & 3); }
 
 // LDS rows are cut in 16-byte chunks, and chunk c of a row sits at c ^
-// swizzle(row) (the xor stays within 16 chunks, 256 bytes).  Two reads have
-// to spread over the banks: 16-byte reads of one chunk of 8 consecutive rows
-// (the low three bits take 8 values), and the transposed reads, whose 16
-// lanes cover 32 bytes (a chunk pair) of 4 consecutive rows (the pair bits
-// take 4 values): so the row's low two bits pick the pair, the third the
-// chunk within it.
+// swizzle(row) (the xor stays within 16 chunks, 256 bytes, all 64 banks).  Two
+// reads have to spread over the banks: 16-byte reads of one chunk of 16
+// consecutive rows, and the transposed reads, of which 32 lanes cover 32 bytes
+// (a chunk pair) of 8 rows, or two neighbouring pairs of 4 rows.  So the row's
+// bits 0, 1 and 2 go to bits 1, 2 and 0 of the pair's number, and bit 3 picks
+// the chunk in it.  (With bits 0 and 1 alone on the pair, two 16-lane groups met in
+// the same banks: half of all LDS cycles were conflicts.)
 __device__ __forceinline__ int swizzle(int row) {
-  return ((row & 3) << 1) | ((row >> 2) & 1) | (row & 8);
+  return ((row & 3) << 2) | ((row >> 1) & 2) | ((row >> 3) & 1);
+}
+
+// LDS reads by byte address.
+template <typename T>
+__device__ __forceinline__ T read_lds(uint32_t at) {
+  typedef const __attribute__((address_space(3))) T* lds_ptr;
+  return *(lds_ptr)at;
 }
 
 // Transposed read: the 16 lanes j of a quarter-wave name 4 rows of 16 16-bit
 // columns, lane j the 8 bytes of row j / 4, columns 4 (j % 4) .. + 3, and lane
 // j gets column j of the 4 rows.
-__device__ __forceinline__ bf16x4 read_tr(const char* lds) {
+__device__ __forceinline__ bf16x4 read_tr(uint32_t at) {
   typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)lds));
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at));
 }
 
 // The same for 8-bit elements: lane j names 8 bytes (columns 8 (j % 2) .. + 7) of
 // row j / 2 of 8, and gets column j of the 8 rows.
-__device__ __forceinline__ uint2 read_tr8(const char* lds) {
+__device__ __forceinline__ u32x2 read_tr8(uint32_t at) {
   typedef int i32x2 __attribute__((ext_vector_type(2)));
   typedef __attribute__((address_space(3))) i32x2* lds_ptr;
-  const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)lds);
-  return make_uint2((uint32_t)v[0], (uint32_t)v[1]);
+  const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)at);
+  return __builtin_bit_cast(u32x2, v);
 }
 
 // Eight E4M3 codes as bf16, exactly.
-__device__ __forceinline__ bf16x8 widen8(uint2 codes) {
+__device__ __forceinline__ bf16x8 widen8(u32x2 codes) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes.x, 1.0f, false);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes.x, 1.0f, true);
   const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes.y, 1.0f, false);
@@ -122,20 +131,29 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // A run of N matrix instructions whose LDS reads are issued D instructions
-// ahead: read(i) gives step i's operand, use(i, operand) multiplies it.  The
-// compiler, left alone with few registers to spare, places each read right in
-// front of its use, and every matrix instruction then waits for the LDS; the
-// scheduling barriers keep the order written here.
+// ahead: read(i) gives what step i takes from LDS, widen() of it the operand
+// (one step ahead, so that no matrix instruction waits for the conversion right
+// before it), use(i, operand) multiplies.  The compiler, left alone with few
+// registers to spare, places each read right in front of its use, and every
+// matrix instruction then waits for the LDS; the scheduling barriers keep the
+// order written here.
+__device__ __forceinline__ bf16x8 widen(bf16x8 rows) { return rows; }
+__device__ __forceinline__ bf16x8 widen(u32x2 codes) { return widen8(codes); }
+
 template <int N, int D, typename Read, typename Use>
 __device__ __forceinline__ void run_ahead(Read read, Use use) {
   decltype(read(0)) held[D];
 #pragma unroll
   for (int i = 0; i < D; ++i) held[i] = read(i);
   __builtin_amdgcn_sched_barrier(0);
+  bf16x8 operand = widen(held[0]);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    use(i, held[i % D]);
+    bf16x8 next = operand;
+    if (i + 1 < N) next = widen(held[(i + 1) % D]);
+    use(i, operand);
     if (i + D < N) held[i % D] = read(i + D);
+    operand = next;
     __builtin_amdgcn_sched_barrier(0);
   }
 }

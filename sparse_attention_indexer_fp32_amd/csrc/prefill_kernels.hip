@@ -199,6 +199,7 @@ template <bool MASKED>
 __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const TileReads& at, int limit,
                                             float scale_log2, int lane) {
   const int hb = lane >> 5;
+  const uint32_t stage = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)t.up;
   f32x16 s[2];
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
@@ -240,7 +241,7 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
       const float w = __builtin_amdgcn_exp2f(fmaf(s[kb][r], scale_log2, -st.m));
       st.l += w;
       if (MASKED) s[kb][r] = w;
-      p[2 * kb + (r >> 3)][r & 7] = (__bf16)w;
+      p[2 * kb + ((r >> 2) & 1)][((r >> 3) << 2) + (r & 3)] = (__bf16)w;   // a step: rows 0..3 and 16..19 of each half
     }
   if (MASKED && values_not_finite(t, here(lane))) {
     add_values_one_by_one(st.o, s, t, limit, here(lane));
@@ -250,9 +251,9 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
   for (int k = 0; k < 4; ++k)
 #pragma unroll
     for (int cb = 0; cb < kColBlocks; ++cb) {
-      // rows 8 further swizzle with bit 3 flipped: the offset of column block cb ^ 2
-      const char* v = t.up + 16 * k * kUpBytes;
-      st.o[cb] = mfma(join8(read_tr(v + at.value[cb]), read_tr(v + 8 * kUpBytes + at.value[cb ^ 2])), p[k], st.o[cb]);
+      // step k: rows 32 (k / 2) + 8 (k % 2) + 4 hb + 0..3 and those 16 on; rows 8 on swizzle with bit 0 flipped
+      const uint32_t v = stage + 32 * (k >> 1) * kUpBytes + 8 * (k & 1) * kUpBytes + (at.value[cb] ^ (uint32_t)((k & 1) << 4));
+      st.o[cb] = mfma(join8(read_tr(v), read_tr(v + 16 * kUpBytes)), p[k], st.o[cb]);
     }
 }
 
