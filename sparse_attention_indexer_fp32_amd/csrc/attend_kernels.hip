@@ -7,8 +7,8 @@
 //
 // One pass over the rows with a running reference maximum and sum per head.
 //
-// Tiling.  A wave owns 16 heads, a workgroup 1, 2, 4 or 8 waves (up to 128
-// heads); a tile is 32 keys.  Both products are taken transposed,
+// Tiling.  A wave owns 16 heads, a workgroup 1, 2 or 4 waves (more than 64
+// heads take several workgroups); a tile is 32 keys.  Both products are taken transposed,
 //   S^T = K Q^T   (rows: keys,          columns: heads; 18 steps of 32 values),
 //   O^T = V^T P^T (rows: latent values, columns: heads; one step of 32 keys),
 // so that a lane keeps one head throughout: its column of S^T, that head's
@@ -54,21 +54,23 @@ constexpr int kTileRope = kTileKeys * kRopeBytes;
 __device__ __attribute__((aligned(16))) const char kZeroRow[kRowBytes] = {};
 
 // A workgroup's LDS: a ring of stages (one tile's rows as they are loaded), the
-// keys' scales (E4M3) and the tiles' list entries.  Two workgroups of up to 64
-// heads share a CU, with one bf16 tile or two of codes on their way while one is
-// computed; 128 heads take all of a CU's registers.
+// keys' scales (E4M3) and the tiles' list entries.  Two workgroups share a CU,
+// with one bf16 tile or two of codes on their way while one is computed.  (One
+// workgroup of 128 heads to a CU keeps its 8 waves in step: 1024 tokens x 128
+// heads x 2048 slots took 778 us against 2 x 435 of 64 heads, or 704 against 2
+// x 310 without the loads.)
 template <int NW, bool E4M3>
 struct Lds {
   static constexpr int kLatentBytes = E4M3 ? kTileCodes : kTileLatent;
   static constexpr int kStageBytes = kLatentBytes + kTileRope;
-  static constexpr int kAhead = NW < 8 && !E4M3 ? 1 : 2;                      // tiles on their way
+  static constexpr int kAhead = E4M3 ? 2 : 1;                                 // tiles on their way
   static constexpr int kStages = kAhead + 1;
   static constexpr int kScales = kStages * kStageBytes;                       // a wave's own: 32 a stage
   static constexpr int kEntries = kScales + (E4M3 ? NW * kStages * 128 : 0);  // a wave's own: two tiles
   static constexpr int kBytes = kEntries + (kAhead > 1 ? NW * 2 * 128 : 0);
-  static_assert(!E4M3 || kAhead > 1, "scales are loaded into LDS");
-  // loads of rows a wave queues per tile, at least
-  static constexpr int kLoads = (E4M3 ? kTileKeys / 2 : kTileKeys) / NW + (NW <= 4 ? 4 / NW : 0);
+  static_assert(2 * kBytes <= 160 * 1024, "two workgroups to a CU");
+  // loads of rows a wave queues per tile
+  static constexpr int kLoads = (E4M3 ? kTileKeys / 2 : kTileKeys) / NW + 4 / NW;
 };
 
 // What a wave keeps of its 16 heads along a row of keys.
@@ -164,8 +166,7 @@ __device__ __forceinline__ void load_tile(const Cache& c, int slots, uint32_t ld
     }
   }
   lds += E4M3 ? kTileCodes : kTileLatent;
-  constexpr int kRopeEach = NW < 4 ? 4 / NW : 1;   // eight rows an instruction
-  if (NW > 4 && wave >= 4) return;
+  constexpr int kRopeEach = 4 / NW;             // eight rows an instruction
 #pragma unroll
   for (int i = 0; i < kRopeEach; ++i) {
     const int group = wave * kRopeEach + i;
@@ -377,9 +378,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
   const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int head = (blockIdx.y * NW + wave) * kHeads + (lane & 15), group = lane >> 4;
-  const bool live_wave = (int)(blockIdx.y * NW + wave) * kHeads < a.num_heads;
+  // Workgroups are dealt to the 8 XCDs in turn.  The head blocks of the same keys
+  // follow each other on one XCD, so that all but the first find the rows in its L2.
+  const int blocks = (a.num_heads + kHeads * NW - 1) / (kHeads * NW);
+  const int xcd = blockIdx.x & 7, nth = (int)(blockIdx.x >> 3) / blocks, block = (int)(blockIdx.x >> 3) % blocks;
+  const int head = (block * NW + wave) * kHeads + (lane & 15), group = lane >> 4;
+  const bool live_wave = (block * NW + wave) * kHeads < a.num_heads;
   const bool split = a.wgs > 0;
+  const int share = nth * 8 + xcd;      // split: this workgroup's number among those of its head block
 
   // this workgroup's tiles [lo, hi) of all tokens' tiles, beginning in token
   // t, whose first tile is number `start` and whose request is b
@@ -392,9 +398,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
       plan_split<NW>(a, plan, tid);
       total = __builtin_amdgcn_readfirstlane(plan.start[a.num_tokens]);
       wgs = (int)(a.wgs < total ? a.wgs : total);
-      if ((int)blockIdx.x >= wgs) return;
-      lo = total * blockIdx.x / wgs;
-      hi = total * (blockIdx.x + 1) / wgs;
+      if (share >= wgs) return;
+      lo = total * share / wgs;
+      hi = total * (share + 1) / wgs;
       int l = 0, h = a.num_tokens;
       while (h - l > 1) {
         const int mid = (l + h) >> 1;
@@ -406,18 +412,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
     } else {
       total = a.num_tokens * k_tiles;
       wgs = (int)(a.wgs < total ? a.wgs : total);
-      if ((int)blockIdx.x >= wgs) return;
-      lo = total * blockIdx.x / wgs;
-      hi = total * (blockIdx.x + 1) / wgs;
+      if (share >= wgs) return;
+      lo = total * share / wgs;
+      hi = total * (share + 1) / wgs;
       t = lo / k_tiles;
       start = t * k_tiles;
     }
   } else {
-    // neighbouring tokens select neighbouring rows: each XCD (workgroups are
-    // dealt to the 8 of them in turn) takes a contiguous share of the tokens
+    // neighbouring tokens select neighbouring rows: each XCD takes a contiguous
+    // share of the tokens
     const int64_t per = ((int64_t)a.num_tokens + 7) / 8;
-    t = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || t >= a.num_tokens) return;
+    t = xcd * per + nth;
+    if (nth >= per || t >= a.num_tokens) return;
     if (PAGED && t >= (int64_t)a.q_starts[a.num_requests]) return;
     if (PAGED) b = count_starts(a.q_starts, a.num_requests, t, lane);
   }
@@ -537,25 +543,25 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
         }
         if (a.lse && group == 0) a.lse[row] = l > 0.f ? (st.m + __log2f(l)) * kLn2 : -INFINITY;
       }
-      if (split && tid == 0 && blockIdx.y == 0) {
+      if (split && tid == 0 && block == 0) {
         a.part_rec[2 * t] = 0;
         a.part_rec[2 * t + 1] = 1;
       }
     } else {
       // a part that begins its token is this workgroup's last, any other its first
-      const int64_t slot = first == 0 ? a.wgs + blockIdx.x : blockIdx.x;
-      const int64_t at = ((int64_t)blockIdx.y * 2 * a.wgs + slot) * NW + wave;
+      const int64_t slot = first == 0 ? a.wgs + share : share;
+      const int64_t at = ((int64_t)block * 2 * a.wgs + slot) * NW + wave;
       if (live_wave) {
         float* o = a.part_out + at * (kHeads * kLatent) + lane * 4;
 #pragma unroll
         for (int cb = 0; cb < kColBlocks; ++cb) *reinterpret_cast<f32x4*>(o + cb * 256) = st.o[cb];
         if (group == 0) a.part_ml[at * kHeads + lane] = make_float2(st.m, l);
       }
-      if (first == 0 && tid == 0 && blockIdx.y == 0) {
+      if (first == 0 && tid == 0 && block == 0) {
         // the last of its tiles is held by the last workgroup g with total g / wgs <= that tile
         const int64_t g1 = ((start + n) * wgs - 1) / total;
-        a.part_rec[2 * t] = (int32_t)blockIdx.x;
-        a.part_rec[2 * t + 1] = (int32_t)(g1 - blockIdx.x + 1);
+        a.part_rec[2 * t] = share;
+        a.part_rec[2 * t + 1] = (int32_t)(g1 - share + 1);
       }
     }
     if (!split) return;
@@ -651,14 +657,16 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttendArgs a) {
   if (a.lse && cb0 == 0 && group == 0) a.lse[row] = st.l > 0.f ? (st.m + __log2f(st.l)) * kLn2 : -INFINITY;
 }
 
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
+int ceil_div(int a, int b) { return (int)(((int64_t)a + b - 1) / b); }
 
 template <int NW, bool E4M3>
 hipError_t launch(const AttendArgs& a, hipStream_t stream) {
-  const unsigned x = a.wgs > 0 ? (unsigned)a.wgs : (unsigned)(((int64_t)a.num_tokens + 7) / 8 * 8);
-  const dim3 grid(x, (unsigned)ceil_div(a.num_heads, kHeads * NW)), block(64 * NW);
+  const int64_t shares = ceil_div(a.wgs > 0 ? a.wgs : a.num_tokens, 8);
+  const int64_t x = shares * 8 * ceil_div(a.num_heads, kHeads * NW);
+  if (x > (int64_t)INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)x), block(64 * NW);
   constexpr int kLds = Lds<NW, E4M3>::kBytes;
-  static_assert(kLds <= 160 * 1024 && sizeof(SplitPlan) <= (size_t)kLds, "LDS of a workgroup");
+  static_assert(sizeof(SplitPlan) <= (size_t)kLds, "the plan is made where the rows go");
   auto* kernel = a.indices ? attend_kernel<NW, E4M3, false> : attend_kernel<NW, E4M3, true>;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
@@ -675,8 +683,7 @@ hipError_t launch_heads(const AttendArgs& a, hipStream_t stream) {
   switch (attend_waves(a.num_heads)) {
     case 1: return launch<1, E4M3>(a, stream);
     case 2: return launch<2, E4M3>(a, stream);
-    case 4: return launch<4, E4M3>(a, stream);
-    default: return launch<8, E4M3>(a, stream);
+    default: return launch<4, E4M3>(a, stream);
   }
 }
 
@@ -684,12 +691,10 @@ hipError_t launch_heads(const AttendArgs& a, hipStream_t stream) {
 
 int attend_waves(int num_heads) {
   const int groups = ceil_div(num_heads, kHeads);
-  return groups <= 1 ? 1 : (groups <= 2 ? 2 : (groups <= 4 ? 4 : 8));
+  return groups <= 1 ? 1 : (groups <= 2 ? 2 : 4);
 }
 
 int attend_heads(int num_heads) { return kHeads * attend_waves(num_heads); }
-
-int attend_per_cu(int num_heads) { return attend_waves(num_heads) < 8 ? 2 : 1; }
 
 SplitLayout split_layout(int num_tokens, int num_heads, int wgs) {
   const int nw = attend_waves(num_heads);

@@ -96,7 +96,7 @@ float scale_log2(float softmax_scale) {
 int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, int32_t num_requests) {
   const int heads = latent::attend_heads(num_heads);
   const int64_t blocks = (num_heads + heads - 1) / heads;
-  const int64_t resident = (int64_t)cus * latent::attend_per_cu(num_heads);
+  const int64_t resident = (int64_t)cus * latent::kAttendPerCu;
   if (num_tokens > latent::kSplitTokens || num_requests > 65535 || num_tokens * blocks >= 4 * resident) return 0;
   int64_t wgs = resident / blocks;
   const int64_t tiles = num_tokens * ((keys + latent::kTileKeys - 1) / latent::kTileKeys + 1);

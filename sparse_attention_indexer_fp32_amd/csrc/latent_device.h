@@ -33,15 +33,20 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
 __device__ __forceinline__ int acc_row(int r, int hb) { return 8 * (r >> 2) + 4 * hb + (r & 3); }
 
 // LDS rows are cut in 16-byte chunks, and chunk c of a row sits at c ^
-// swizzle(row) (the xor stays within 16 chunks, 256 bytes, all 64 banks).  Two
-// reads have to spread over the banks: 16-byte reads of one chunk of 16
-// consecutive rows, and the transposed reads, of which 32 lanes cover 32 bytes
-// (a chunk pair) of 8 rows, or two neighbouring pairs of 4 rows.  So the row's
-// bits 0, 1 and 2 go to bits 1, 2 and 0 of the pair's number, and bit 3 picks
-// the chunk in it.  (With bits 0 and 1 alone on the pair, two 16-lane groups met in
-// the same banks: half of all LDS cycles were conflicts.)
+// swizzle(row) (the xor stays within 16 chunks: 256 bytes, all 64 banks).  Reads
+// that have to spread over the banks:
+//   * 16 bytes a lane, 16 lanes at a time, lanes 0..3, 12..15, 20..23, 24..27 of a
+//     half-wave and the rest: with lane = row that is 16 rows of one chunk, any
+//     one-to-one map; with lane = 16 g + row and chunk c + g, rows 0..3 and
+//     12..15 of c and rows 4..11 of c + 1, so a row's partner within a chunk
+//     pair has to be row ^ 12;
+//   * transposed, 32 lanes at a time: a chunk pair of 8 rows, or two neighbouring pairs of
+//     4 rows, so rows differ in the pair's number, bits 0 and 1 of the row in
+//     its upper two bits.
+// Both hold for this linear map.  (A map that missed the second lost half of all LDS
+// cycles to conflicts, one that missed the first a quarter.)
 __device__ __forceinline__ int swizzle(int row) {
-  return ((row & 3) << 2) | ((row >> 1) & 2) | ((row >> 3) & 1);
+  return ((row & 3) << 2) ^ ((row >> 1) & 2) ^ ((row >> 3) & 1) * 3;
 }
 
 // LDS reads by byte address.

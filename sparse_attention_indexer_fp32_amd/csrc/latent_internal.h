@@ -109,11 +109,11 @@ struct AttendArgs {
   int32_t* part_rec;
 };
 
-// By head count: waves of a workgroup, heads it takes, workgroups a CU holds;
-// and the workspace of a split launch.
+// Workgroups a CU holds; by head count, the waves of a workgroup and the heads it
+// takes; and the workspace of a split launch.
+constexpr int kAttendPerCu = 2;
 int attend_waves(int num_heads);
 int attend_heads(int num_heads);
-int attend_per_cu(int num_heads);
 struct SplitLayout {
   size_t out_bytes, ml_bytes, rec_bytes;
   size_t total() const { return out_bytes + ml_bytes + rec_bytes; }

@@ -251,8 +251,8 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
   for (int k = 0; k < 4; ++k)
 #pragma unroll
     for (int cb = 0; cb < kColBlocks; ++cb) {
-      // step k: rows 32 (k / 2) + 8 (k % 2) + 4 hb + 0..3 and those 16 on; rows 8 on swizzle with bit 0 flipped
-      const uint32_t v = stage + 32 * (k >> 1) * kUpBytes + 8 * (k & 1) * kUpBytes + (at.value[cb] ^ (uint32_t)((k & 1) << 4));
+      // step k: rows 32 (k / 2) + 8 (k % 2) + 4 hb + 0..3 and those 16 on; rows 8 on swizzle with bits 0 and 1 flipped
+      const uint32_t v = stage + 32 * (k >> 1) * kUpBytes + 8 * (k & 1) * kUpBytes + (at.value[cb] ^ (uint32_t)((k & 1) * 48));
       st.o[cb] = mfma(join8(read_tr(v), read_tr(v + 16 * kUpBytes)), p[k], st.o[cb]);
     }
 }
