@@ -668,10 +668,8 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream) {
   constexpr int kLds = Lds<NW, E4M3>::kBytes;
   static_assert(sizeof(SplitPlan) <= (size_t)kLds, "the plan is made where the rows go");
   auto* kernel = a.indices ? attend_kernel<NW, E4M3, false> : attend_kernel<NW, E4M3, true>;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a);
-  e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.wgs == 0) return e;
   hipLaunchKernelGGL(join_kernel<NW>, dim3((unsigned)a.num_tokens, (unsigned)ceil_div(a.num_heads, kHeads), kColBlocks / kJoinBlocks),
                      dim3(64 * kJoinWaves), 0, stream, a);

@@ -4,11 +4,9 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstdio>
 #include <cstring>
-#include <map>
-#include <mutex>
-#include <string>
 
 #include "latent_attention.h"
 #include "latent_internal.h"
@@ -16,7 +14,8 @@
 
 namespace {
 
-std::map<int, int> g_cus;   // device -> CUs, 0 when it is not gfx950; under the library's lock
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_cus[kMaxDevices];   // CUs of each device, -1 when it is not gfx950, 0 before it is asked
 
 topk_status_t fail(topk_status_t st, const char* msg) {
   topk::set_last_error(msg);
@@ -37,19 +36,19 @@ topk_status_t launched(hipError_t e, const char* what) {
 
 // CUs of the current device; TOPK_ERROR_UNSUPPORTED when it is not gfx950.
 topk_status_t device_cus(int* cus) {
-  std::lock_guard<std::mutex> lock(topk::lib_mutex());
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return fail(TOPK_ERROR_LAUNCH, "hipGetDevice failed");
-  auto it = g_cus.find(dev);
-  if (it == g_cus.end()) {
+  if (dev < 0 || dev >= kMaxDevices) return fail(TOPK_ERROR_UNSUPPORTED, "device number too large");
+  int n = g_cus[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     hipDeviceProp_t prop;
     if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
       return fail(TOPK_ERROR_LAUNCH, "hipGetDeviceProperties failed");
-    const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    it = g_cus.emplace(dev, ok ? prop.multiProcessorCount : 0).first;
+    n = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? prop.multiProcessorCount : -1;
+    g_cus[dev].store(n, std::memory_order_relaxed);
   }
-  if (it->second == 0) return fail(TOPK_ERROR_UNSUPPORTED, "device is not gfx950");
-  *cus = it->second;
+  if (n < 0) return fail(TOPK_ERROR_UNSUPPORTED, "device is not gfx950");
+  *cus = n;
   return TOPK_SUCCESS;
 }
 

@@ -55,15 +55,22 @@ def declare(lib: ctypes.CDLL) -> None:
         fn.restype = ctypes.c_int
 
 
-def _package():
-    import sparse_attention_indexer_fp32_amd as package
-    return package
+package = torch = None   # this package and torch, once a call has needed them
+
+
+def _modules() -> None:
+    """Binds both names above (they are not imported with this module: the
+    package loads without torch, and imports this module)."""
+    global package, torch
+    import torch as torch_module
+
+    import sparse_attention_indexer_fp32_amd as this_package
+    torch, package = torch_module, this_package
 
 
 @contextlib.contextmanager
 def _on(dev, stream):
     """The tensors' device made current and, for allocations, the call's stream."""
-    import torch
     with torch.cuda.device(dev):
         if stream is None:
             yield
@@ -75,8 +82,6 @@ def _on(dev, stream):
 def _call(name: str, dev, stream, make_args):
     """Calls an entry point on its device; make_args(stream handle) gives its
     arguments and allocates what the caller did not pass."""
-    import torch
-    package = _package()
     fn = getattr(package.load(), name)
     if stream is None and dev.index == torch.cuda.current_device():
         st = fn(*make_args(package._stream_handle(None, dev)))
@@ -86,38 +91,35 @@ def _call(name: str, dev, stream, make_args):
     package._check(st)
 
 
-def _need(ok: bool, text: str) -> None:
-    if not ok:
-        raise ValueError(text)
-
-
 def _int32(name: str, t, shape, dev) -> None:
-    import torch
-    _need(t.dtype == torch.int32 and tuple(t.shape) == shape and t.is_contiguous() and t.device == dev,
-          f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}")
+    if not (t.dtype == torch.int32 and tuple(t.shape) == shape and t.is_contiguous() and t.device == dev):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}")
 
 
 def _gpu(t, name: str):
-    _need(t.device.type == "cuda", f"{name} must be on a GPU")
+    if torch is None:
+        _modules()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
     return t.device
 
 
 def _cache(latent, rope, scale, dev):
     """The cache arguments of a call, and the number of slots."""
-    import torch
-    _need(latent.dim() == 2 and latent.shape[1] == LATENT_DIM and latent.stride(1) == 1 and latent.device == dev,
-          f"latent must be a (slots, {LATENT_DIM}) tensor with contiguous rows on {dev}")
+    if not (latent.dim() == 2 and latent.shape[1] == LATENT_DIM and latent.stride(1) == 1 and latent.device == dev):
+        raise ValueError(f"latent must be a (slots, {LATENT_DIM}) tensor with contiguous rows on {dev}")
     slots = latent.shape[0]
-    _need(rope.dim() == 2 and tuple(rope.shape) == (slots, LATENT_ROPE_DIM) and rope.dtype == torch.bfloat16
-          and rope.stride(1) == 1 and rope.device == dev,
-          f"rope must be a (slots, {LATENT_ROPE_DIM}) bfloat16 tensor with contiguous rows on latent's device")
+    if not (rope.dim() == 2 and tuple(rope.shape) == (slots, LATENT_ROPE_DIM) and rope.dtype == torch.bfloat16
+          and rope.stride(1) == 1 and rope.device == dev):
+        raise ValueError(f"rope must be a (slots, {LATENT_ROPE_DIM}) bfloat16 tensor with contiguous rows on latent's device")
     if scale is None:
-        _need(latent.dtype == torch.bfloat16, "latent must be bfloat16, or uint8 (fp8 E4M3 codes) with scale")
+        if latent.dtype != torch.bfloat16:
+            raise ValueError("latent must be bfloat16, or uint8 (fp8 E4M3 codes) with scale")
         kind, sp = _BF16, None
     else:
-        _need(latent.dtype == torch.uint8 and scale.dtype == torch.float32 and tuple(scale.shape) == (slots,)
-              and scale.is_contiguous() and scale.device == dev,
-              "an 8-bit cache is latent uint8 (fp8 E4M3 codes) and scale, a contiguous (slots,) float32 tensor on its device")
+        if not (latent.dtype == torch.uint8 and scale.dtype == torch.float32 and tuple(scale.shape) == (slots,)
+              and scale.is_contiguous() and scale.device == dev):
+            raise ValueError("an 8-bit cache is latent uint8 (fp8 E4M3 codes) and scale, a contiguous (slots,) float32 tensor on its device")
         kind, sp = _E4M3, scale.data_ptr()
     # a single row has no stride to speak of
     ls = latent.stride(0) if slots > 1 else LATENT_DIM
@@ -126,9 +128,8 @@ def _cache(latent, rope, scale, dev):
 
 
 def _queries(q, width: int):
-    import torch
-    _need(q.dim() == 3 and q.shape[2] == width and q.dtype == torch.bfloat16 and (q.stride(2) == 1 or q.numel() == 0),
-          f"q must be a (tokens, heads, {width}) bfloat16 tensor whose last dimension is contiguous")
+    if not (q.dim() == 3 and q.shape[2] == width and q.dtype == torch.bfloat16 and (q.stride(2) == 1 or q.numel() == 0)):
+        raise ValueError(f"q must be a (tokens, heads, {width}) bfloat16 tensor whose last dimension is contiguous")
     tokens, heads = q.shape[0], q.shape[1]
     return tokens, heads, (q.data_ptr(), q.stride(0) if tokens > 1 else heads * width,
                            q.stride(1) if heads > 1 else width)
@@ -136,17 +137,17 @@ def _queries(q, width: int):
 
 def _outputs(out, lse, tokens: int, heads: int, width: int, dev):
     """Checks the outputs that are passed; those that are not are made by _made."""
-    import torch
     if out is not None:
-        _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (tokens, heads, width) and out.is_contiguous()
-              and out.device == dev, f"out must be a contiguous bfloat16 tensor of shape ({tokens}, {heads}, {width})")
+        if not (out.dtype == torch.bfloat16 and tuple(out.shape) == (tokens, heads, width) and out.is_contiguous()
+              and out.device == dev):
+            raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({tokens}, {heads}, {width})")
     if lse is not None:
-        _need(lse.dtype == torch.float32 and tuple(lse.shape) == (tokens, heads) and lse.is_contiguous()
-              and lse.device == dev, f"lse must be a contiguous float32 tensor of shape ({tokens}, {heads})")
+        if not (lse.dtype == torch.float32 and tuple(lse.shape) == (tokens, heads) and lse.is_contiguous()
+              and lse.device == dev):
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape ({tokens}, {heads})")
 
 
 def _made(out, lse, tokens: int, heads: int, width: int, dev):
-    import torch
     if out is None:
         out = torch.empty((tokens, heads, width), dtype=torch.bfloat16, device=dev)
     if lse is None:
@@ -156,7 +157,6 @@ def _made(out, lse, tokens: int, heads: int, width: int, dev):
 
 @functools.lru_cache(maxsize=4096)
 def _workspace_bytes(device_index: int, tokens: int, heads: int, keys: int) -> int:
-    package = _package()
     n = ctypes.c_size_t(0)
     package._check(package.load().latent_attention_workspace(tokens, heads, keys, ctypes.byref(n)))
     return n.value
@@ -164,7 +164,6 @@ def _workspace_bytes(device_index: int, tokens: int, heads: int, keys: int) -> i
 
 def _workspace(dev, tokens: int, heads: int, keys: int):
     """The workspace of a call as (tensor to hold on to, pointer, bytes)."""
-    import torch
     n = _workspace_bytes(dev.index, tokens, heads, keys)
     if n == 0:
         return None, None, 0
@@ -183,28 +182,31 @@ def paged_append_plan(kv_lens, new_lens, page_table, free_pages, page_size: int,
     tokens are -1.  Returns AppendPlan; free_used above F says that pages ran
     out (their entries and slots are -1).
     """
-    import torch
     dev = _gpu(kv_lens, "kv_lens")
-    B = kv_lens.shape[0]
+    B = kv_lens.numel()
     _int32("kv_lens", kv_lens, (B,), dev)
     _int32("new_lens", new_lens, (B,), dev)
-    _need(page_table.dim() == 2 and page_table.shape[0] == B, "page_table must be (requests, pages)")
+    if not (page_table.dim() == 2 and page_table.shape[0] == B):
+        raise ValueError("page_table must be (requests, pages)")
     _int32("page_table", page_table, tuple(page_table.shape), dev)
-    _need(free_pages.dim() == 1, "free_pages must be 1-D")
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be 1-D")
     _int32("free_pages", free_pages, tuple(free_pages.shape), dev)
     if free_used is not None:
         _int32("free_used", free_used, (1,), dev)
     num_tokens = int(num_tokens)
-    _need(num_tokens >= 0, "num_tokens must be >= 0")
+    if num_tokens < 0:
+        raise ValueError("num_tokens must be >= 0")
     plan = []
 
     def args(handle):
-        new = lambda n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
-        plan.append(AppendPlan(new(B), new(B + 1), new(num_tokens), new(num_tokens), new(1)))
-        p = plan[0]
+        # one allocation for all: these calls take microseconds
+        whole = torch.empty(2 * B + 2 + 2 * num_tokens, dtype=torch.int32, device=dev)
+        plan.append(AppendPlan(*whole.split_with_sizes((B, B + 1, num_tokens, num_tokens, 1))))
+        at = whole.data_ptr()
         return (kv_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), free_pages.data_ptr(),
-                free_used.data_ptr() if free_used is not None else None, int(page_size), p.seq_lens.data_ptr(),
-                p.q_starts.data_ptr(), p.slot_map.data_ptr(), p.positions.data_ptr(), p.free_used.data_ptr(), handle,
+                free_used.data_ptr() if free_used is not None else None, int(page_size), at, at + 4 * B,
+                at + 4 * (2 * B + 1), at + 4 * (2 * B + 1 + num_tokens), at + 4 * (2 * B + 1 + 2 * num_tokens), handle,
                 B, page_table.shape[1], free_pages.shape[0], num_tokens)
 
     _call("paged_append_plan", dev, stream, args)
@@ -223,23 +225,23 @@ def latent_cache_store(kv, slot_map, latent, rope, scale=None, norm_weight=None,
     norm_weight (512,) bfloat16; positions (T,) int32; cos_sin (positions, 64)
     float32: cosines, then sines, of a position's 32 angles.
     """
-    import torch
     dev = _gpu(kv, "kv")
-    _need(kv.dim() == 2 and kv.shape[1] == _QUERY and kv.dtype == torch.bfloat16 and kv.stride(1) == 1,
-          f"kv must be a (tokens, {_QUERY}) bfloat16 tensor with contiguous rows")
+    if not (kv.dim() == 2 and kv.shape[1] == _QUERY and kv.dtype == torch.bfloat16 and kv.stride(1) == 1):
+        raise ValueError(f"kv must be a (tokens, {_QUERY}) bfloat16 tensor with contiguous rows")
     T = kv.shape[0]
     _int32("slot_map", slot_map, (T,), dev)
     cache, slots = _cache(latent, rope, scale, dev)
     if norm_weight is not None:
-        _need(norm_weight.dtype == torch.bfloat16 and tuple(norm_weight.shape) == (LATENT_DIM,)
-              and norm_weight.is_contiguous() and norm_weight.device == dev,
-              f"norm_weight must be a contiguous bfloat16 tensor of shape ({LATENT_DIM},)")
-    _need((positions is None) == (cos_sin is None), "positions and cos_sin go together")
+        if not (norm_weight.dtype == torch.bfloat16 and tuple(norm_weight.shape) == (LATENT_DIM,)
+              and norm_weight.is_contiguous() and norm_weight.device == dev):
+            raise ValueError(f"norm_weight must be a contiguous bfloat16 tensor of shape ({LATENT_DIM},)")
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("positions and cos_sin go together")
     if cos_sin is not None:
         _int32("positions", positions, (T,), dev)
-        _need(cos_sin.dim() == 2 and cos_sin.shape[1] == LATENT_ROPE_DIM and cos_sin.dtype == torch.float32
-              and cos_sin.is_contiguous() and cos_sin.device == dev,
-              f"cos_sin must be a contiguous (positions, {LATENT_ROPE_DIM}) float32 tensor")
+        if not (cos_sin.dim() == 2 and cos_sin.shape[1] == LATENT_ROPE_DIM and cos_sin.dtype == torch.float32
+              and cos_sin.is_contiguous() and cos_sin.device == dev):
+            raise ValueError(f"cos_sin must be a contiguous (positions, {LATENT_ROPE_DIM}) float32 tensor")
     rotate = cos_sin is not None
     _call("latent_cache_store", dev, stream, lambda handle: (
         kv.data_ptr(), kv.stride(0) if T > 1 else _QUERY, norm_weight.data_ptr() if norm_weight is not None else None,
@@ -248,14 +250,13 @@ def latent_cache_store(kv, slot_map, latent, rope, scale=None, norm_weight=None,
 
 
 def _load_outputs(out_latent, out_rope, rows: int, dev):
-    import torch
     for name, t, width in (("out_latent", out_latent, LATENT_DIM), ("out_rope", out_rope, LATENT_ROPE_DIM)):
-        _need(t is None or (t.dtype == torch.bfloat16 and tuple(t.shape) == (rows, width) and t.is_contiguous()
-                            and t.device == dev), f"{name} must be a contiguous bfloat16 tensor of shape ({rows}, {width})")
+        if not (t is None or (t.dtype == torch.bfloat16 and tuple(t.shape) == (rows, width) and t.is_contiguous()
+                            and t.device == dev)):
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor of shape ({rows}, {width})")
 
 
 def _load_made(out_latent, out_rope, rows: int, dev):
-    import torch
     if out_latent is None:
         out_latent = torch.empty((rows, LATENT_DIM), dtype=torch.bfloat16, device=dev)
     if out_rope is None:
@@ -268,7 +269,8 @@ def latent_cache_load(slots, latent, rope, scale=None, out_latent=None, out_rope
     """Rows of the cache by slot, as contiguous bfloat16: (rows, 512) and (rows,
     64).  slots (rows,) int32; a slot outside the cache gives zeros."""
     dev = _gpu(slots, "slots")
-    _need(slots.dim() == 1, "slots must be 1-D")
+    if slots.dim() != 1:
+        raise ValueError("slots must be 1-D")
     rows = slots.shape[0]
     _int32("slots", slots, (rows,), dev)
     cache, n = _cache(latent, rope, scale, dev)
@@ -290,12 +292,14 @@ def latent_cache_load_paged(page_table, kv_starts, page_size: int, num_rows: int
     page_table (B, P) int32, kv_starts (B + 1,) int32; num_rows is the length
     of the outputs, and rows past kv_starts[B] are left as they are."""
     dev = _gpu(page_table, "page_table")
-    _need(page_table.dim() == 2, "page_table must be (requests, pages)")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be (requests, pages)")
     B = page_table.shape[0]
     _int32("page_table", page_table, tuple(page_table.shape), dev)
     _int32("kv_starts", kv_starts, (B + 1,), dev)
     rows = int(num_rows)
-    _need(rows >= 0, "num_rows must be >= 0")
+    if rows < 0:
+        raise ValueError("num_rows must be >= 0")
     cache, n = _cache(latent, rope, scale, dev)
     _load_outputs(out_latent, out_rope, rows, dev)
     got = []
@@ -321,7 +325,8 @@ def latent_attention(q, latent, rope, indices, softmax_scale: float, scale=None,
     """
     dev = _gpu(q, "q")
     T, H, qargs = _queries(q, _QUERY)
-    _need(indices.dim() == 2, "indices must be (tokens, k)")
+    if indices.dim() != 2:
+        raise ValueError("indices must be (tokens, k)")
     k = indices.shape[1]
     _int32("indices", indices, (T, k), dev)
     cache, slots = _cache(latent, rope, scale, dev)
@@ -350,7 +355,8 @@ def latent_attention_paged(q, latent, rope, page_table, seq_lens, q_starts, page
     """
     dev = _gpu(q, "q")
     T, H, qargs = _queries(q, _QUERY)
-    _need(page_table.dim() == 2, "page_table must be (requests, pages)")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be (requests, pages)")
     B, P = page_table.shape
     _int32("page_table", page_table, (B, P), dev)
     _int32("seq_lens", seq_lens, (B,), dev)
@@ -380,16 +386,17 @@ def latent_attention_expanded(q, kv_up, rope, q_starts, kv_starts, softmax_scale
     out (Tq, H, 128) bfloat16 and lse (Tq, H) float32; a query with no key
     gets zeros and -inf, rows past q_starts[B] are left as they are.
     """
-    import torch
     dev = _gpu(q, "q")
     T, H, qargs = _queries(q, LATENT_HEAD_DIM + LATENT_ROPE_DIM)
-    _need(kv_up.dim() == 3 and tuple(kv_up.shape[1:]) == (H, 2 * LATENT_HEAD_DIM) and kv_up.dtype == torch.bfloat16
-          and (kv_up.stride(2) == 1 or kv_up.numel() == 0) and kv_up.device == dev,
-          f"kv_up must be a (keys, {H}, {2 * LATENT_HEAD_DIM}) bfloat16 tensor whose last dimension is contiguous")
+    if not (kv_up.dim() == 3 and tuple(kv_up.shape[1:]) == (H, 2 * LATENT_HEAD_DIM) and kv_up.dtype == torch.bfloat16
+          and (kv_up.stride(2) == 1 or kv_up.numel() == 0) and kv_up.device == dev):
+        raise ValueError(f"kv_up must be a (keys, {H}, {2 * LATENT_HEAD_DIM}) bfloat16 tensor whose last dimension is contiguous")
     K = kv_up.shape[0]
-    _need(tuple(rope.shape) == (K, LATENT_ROPE_DIM) and rope.dtype == torch.bfloat16 and rope.stride(1) == 1
-          and rope.device == dev, f"rope must be a ({K}, {LATENT_ROPE_DIM}) bfloat16 tensor with contiguous rows")
-    _need(q_starts.dim() == 1 and q_starts.shape[0] >= 1, "q_starts must be (requests + 1,)")
+    if not (tuple(rope.shape) == (K, LATENT_ROPE_DIM) and rope.dtype == torch.bfloat16 and rope.stride(1) == 1
+          and rope.device == dev):
+        raise ValueError(f"rope must be a ({K}, {LATENT_ROPE_DIM}) bfloat16 tensor with contiguous rows")
+    if not (q_starts.dim() == 1 and q_starts.shape[0] >= 1):
+        raise ValueError("q_starts must be (requests + 1,)")
     B = q_starts.shape[0] - 1
     _int32("q_starts", q_starts, (B + 1,), dev)
     _int32("kv_starts", kv_starts, (B + 1,), dev)
