@@ -54,12 +54,18 @@ constexpr int kTileRope = kTileKeys * kRopeBytes;
 __device__ __attribute__((aligned(16))) const char kZeroRow[kRowBytes] = {};
 
 // A workgroup's LDS: a ring of stages (one tile's rows as they are loaded), the
-// keys' scales (E4M3) and the tiles' list entries.  Two workgroups share a CU,
-// with one bf16 tile or two of codes on their way while one is computed.  (One
-// workgroup of 128 heads to a CU keeps its 8 waves in step: 1024 tokens x 128
-// heads x 2048 slots took 778 us against 2 x 435 of 64 heads, or 704 against 2
-// x 310 without the loads.)
-template <int NW, bool E4M3>
+// keys' scales (E4M3) and the tiles' list entries, with one bf16 tile or two of codes on
+// their way while one is computed.  Two rings fit a CU:
+//   * two workgroups of one ring, when every token has its own (they drift
+//     apart, so one computes while the other waits);
+//   * one workgroup with two rings, whose waves take alternate tiles of the same
+//     part and are joined in LDS at its end, when tokens are split: half the parts to
+//     write out and read back (64 tokens x 64 heads over 2048 8-bit slots: 8
+//     parts of 128 KB a token became 4).
+// (One workgroup of 128 heads keeps its 8 waves in step with one ring: 1024
+// tokens x 128 heads x 2048 slots took 778 us against 2 x 435 of 64 heads, or
+// 704 against 2 x 310 without the loads.)
+template <int NW, int RINGS, bool E4M3>
 struct Lds {
   static constexpr int kLatentBytes = E4M3 ? kTileCodes : kTileLatent;
   static constexpr int kStageBytes = kLatentBytes + kTileRope;
@@ -67,8 +73,11 @@ struct Lds {
   static constexpr int kStages = kAhead + 1;
   static constexpr int kScales = kStages * kStageBytes;                       // a wave's own: 32 a stage
   static constexpr int kEntries = kScales + (E4M3 ? NW * kStages * 128 : 0);  // a wave's own: two tiles
-  static constexpr int kBytes = kEntries + (kAhead > 1 ? NW * 2 * 128 : 0);
-  static_assert(2 * kBytes <= 160 * 1024, "two workgroups to a CU");
+  static constexpr int kRingBytes = (kEntries + (kAhead > 1 ? NW * 2 * 128 : 0) + 255) / 256 * 256;
+  // joining: the second ring's waves' accumulators, then their maxima and sums
+  static constexpr int kJoinBytes = RINGS > 1 ? NW * (kHeads * kLatent * 4 + 512) : 0;
+  static constexpr int kBytes = RINGS * kRingBytes > kJoinBytes ? RINGS * kRingBytes : kJoinBytes;
+  static_assert(2 / RINGS * kBytes <= 160 * 1024, "two rings to a CU");
   // loads of rows a wave queues per tile
   static constexpr int kLoads = (E4M3 ? kTileKeys / 2 : kTileKeys) / NW + 4 / NW;
 };
@@ -80,6 +89,12 @@ struct HeadState {
   float m;      // reference maximum (log2 units)
   float l;      // this lane's part of the sum
 };
+
+// Of a split launch's workgroups, those that take part.
+__device__ __forceinline__ int shares_of(const AttendArgs& a, int64_t tiles) {
+  const int64_t most = tiles / kShareTiles;
+  return most < 1 ? 1 : most < a.wgs ? (int)most : a.wgs;
+}
 
 // Where the keys of a token come from.
 struct TokenKeys {
@@ -172,7 +187,7 @@ __device__ __forceinline__ void load_tile(const Cache& c, int slots, uint32_t ld
     const int group = wave * kRopeEach + i;
     const int s = __builtin_amdgcn_ds_bpermute((group * 8 + (lane >> 3)) * 4, slots);
     const char* row = row_at(c.rope, c.rope_stride, s);
-    queue_to_lds(row + ((lane ^ (lane >> 3)) & 7) * 16, lds + group * 8 * kRopeBytes);
+    queue_to_lds(row + ((lane ^ ((group * 8 + (lane >> 3)) >> 1)) & 7) * 16, lds + group * 8 * kRopeBytes);
   }
 }
 
@@ -191,7 +206,7 @@ template <bool E4M3>
 __device__ __forceinline__ TileReads tile_reads(int lane) {
   const int i = lane & 15, g = lane >> 4;
   TileReads t;
-  t.rope = i * kRopeBytes + (((g ^ i) & 7) << 4);
+  t.rope = i * kRopeBytes + (((g ^ (i >> 1)) & 7) << 4);
   if (E4M3) {
     const int key = 4 * g + ((i >> 1) & 3) + 16 * (i >> 3);
     t.key = i * kLatent + (((g >> 1) ^ code_swizzle(i)) << 4) + (g & 1) * 8;
@@ -208,7 +223,7 @@ __device__ __forceinline__ TileReads tile_reads(int lane) {
 // 16 b + 4 (lane / 16) + r.  scales (E4M3): each key's scale.  (Stages begin at
 // multiples of 256 bytes, so their address may be added before the xor.)
 template <bool E4M3>
-__device__ __forceinline__ void score_tile(const HeadState& st, f32x4 (&s)[2], uint32_t lat, const float* scales,
+__device__ __forceinline__ void score_tile(const HeadState& st, f32x4 (&s)[2], uint32_t lat, uint32_t scales,
                                            const TileReads& at, int lane) {
   s[0] = f32x4{};
   s[1] = f32x4{};
@@ -223,7 +238,7 @@ __device__ __forceinline__ void score_tile(const HeadState& st, f32x4 (&s)[2], u
         [&](int n, bf16x8 rows) { s[n & 1] = mfma16(rows, st.q[n >> 1], s[n & 1]); });
     const int g = lane >> 4;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) s[b] *= *reinterpret_cast<const f32x4*>(scales + 16 * b + 4 * g);
+    for (int b = 0; b < 2; ++b) s[b] *= read_lds<f32x4>(scales + 64 * b + 16 * g);
   } else {
     run_ahead<2 * kLatentSteps, kReadsAhead>(
         [&](int n) {
@@ -241,7 +256,7 @@ __device__ __forceinline__ void score_tile(const HeadState& st, f32x4 (&s)[2], u
 // The softmax step and the second product of a tile whose scores are s.
 // mask: the tile's selected keys.
 template <bool E4M3>
-__device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], uint32_t lat, const float* scales,
+__device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], uint32_t lat, uint32_t scales,
                                            uint32_t mask, float scale_log2, const TileReads& at, int lane) {
   const int g = lane >> 4;
   if (mask != 0xFFFFFFFFu) {
@@ -275,7 +290,7 @@ __device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], uint32_
 #pragma unroll
     for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], scale_log2, -st.m));
     st.l += (w[0] + w[1]) + (w[2] + w[3]);
-    if (E4M3) w *= *reinterpret_cast<const f32x4*>(scales + 16 * b + 4 * g);
+    if (E4M3) w *= read_lds<f32x4>(scales + 64 * b + 16 * g);
 #pragma unroll
     for (int r = 0; r < 4; ++r) p[4 * b + r] = (__bf16)w[r];
   }
@@ -316,8 +331,8 @@ __device__ __forceinline__ int64_t token_len(const AttendArgs& a, int64_t t, int
 
 // A split launch's plan of whole sequences: the tiles before each token, and its request.
 struct SplitPlan {
-  int32_t start[kSplitTokens + 1];
-  uint16_t request[kSplitTokens];
+  int32_t start[kPlanTokens + 1];
+  uint16_t request[kPlanTokens];
 };
 
 // A token's tiles; one even when it has no key, so that somebody writes its row.
@@ -371,20 +386,20 @@ __device__ void plan_split(const AttendArgs& a, SplitPlan& plan, int tid) {
   lds_barrier();
 }
 
-template <int NW, bool E4M3, bool PAGED>
-__global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
-  using L = Lds<NW, E4M3>;
+template <int NW, int RINGS, bool E4M3, bool PAGED>
+__global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a) {
+  using L = Lds<NW, RINGS, E4M3>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % NW, ring = __builtin_amdgcn_readfirstlane(tid >> 6) / NW;
+  const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + ring * L::kRingBytes;
   // Workgroups are dealt to the 8 XCDs in turn.  The head blocks of the same keys
   // follow each other on one XCD, so that all but the first find the rows in its L2.
   const int blocks = (a.num_heads + kHeads * NW - 1) / (kHeads * NW);
   const int xcd = blockIdx.x & 7, nth = (int)(blockIdx.x >> 3) / blocks, block = (int)(blockIdx.x >> 3) % blocks;
   const int head = (block * NW + wave) * kHeads + (lane & 15), group = lane >> 4;
   const bool live_wave = (block * NW + wave) * kHeads < a.num_heads;
-  const bool split = a.wgs > 0;
+  constexpr bool split = RINGS > 1;
   const int share = nth * 8 + xcd;      // split: this workgroup's number among those of its head block
 
   // this workgroup's tiles [lo, hi) of all tokens' tiles, beginning in token
@@ -395,9 +410,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
   if (split) {
     if (PAGED) {
       SplitPlan& plan = *reinterpret_cast<SplitPlan*>(lds);
-      plan_split<NW>(a, plan, tid);
+      plan_split<NW * RINGS>(a, plan, tid);
       total = __builtin_amdgcn_readfirstlane(plan.start[a.num_tokens]);
-      wgs = (int)(a.wgs < total ? a.wgs : total);
+      wgs = shares_of(a, total);
       if (share >= wgs) return;
       lo = total * share / wgs;
       hi = total * (share + 1) / wgs;
@@ -411,7 +426,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
       b = __builtin_amdgcn_readfirstlane((int)plan.request[t]);
     } else {
       total = a.num_tokens * k_tiles;
-      wgs = (int)(a.wgs < total ? a.wgs : total);
+      wgs = shares_of(a, total);
       if (share >= wgs) return;
       lo = total * share / wgs;
       hi = total * (share + 1) / wgs;
@@ -463,74 +478,97 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
       }
     }
 
-    // Tiles past the part's last selected key hold nothing (a short row's tail).
-    const int64_t end = PAGED ? (tk.len > 0 ? last : first) : first + selected_tiles(a, tk, first, last, lane);
-    // The ring: tile i is in stage (i - first) % kStages; masks[d], the
-    // selected keys of the tile d after the one being computed.  A tile's list
-    // entries are loaded one tile before its rows.  With two tiles on their
-    // way, entries and scales too are loaded into LDS, so that no load in the
-    // loop is the compiler's to wait for.
+    // The ring: this wave's tiles are first + ring + RINGS i, tile i in stage i %
+    // kStages; masks[d], the selected keys of the tile d after the one being
+    // computed.  A tile's list entries are loaded one tile before its rows.
+    // With two tiles on their way, entries and scales too are loaded into LDS,
+    // so that no load in the loop is the compiler's to wait for.
     uint32_t masks[L::kAhead + 1];
     int entry = 0;                        // kAhead == 1: of the tile to be queued next
     int into = 0;                         // the stage of the tile to be queued next
-    const char* own_entries = lds + L::kEntries + wave * 256;
-    const float* scales = reinterpret_cast<const float*>(lds + L::kScales + wave * L::kStages * 128);
-    lds_barrier();                        // the last part's reads are done
-    auto load_entries = [&](int64_t tile) {
-      const int32_t* at = entry_of<PAGED>(a, tk, tile);
+    const uint32_t own_entries = lds_base + L::kEntries + wave * 256;
+    const uint32_t scales = lds_base + L::kScales + wave * L::kStages * 128;
+    auto tile_of = [&](int i) { return first + ring + RINGS * i; };
+    auto load_entries = [&](int i) {
+      const int32_t* at = entry_of<PAGED>(a, tk, tile_of(i));
       if (L::kAhead > 1)
-        queue_words_to_lds(at, lds_base + L::kEntries + wave * 256 + (uint32_t)(tile & 1) * 128);
+        queue_words_to_lds(at, own_entries + (uint32_t)(i & 1) * 128);
       else
         entry = *at;
     };
-    auto queue = [&](int64_t tile, uint32_t& mask) {
-      if (L::kAhead > 1) entry = *reinterpret_cast<const int*>(own_entries + (tile & 1) * 128 + (lane_here() & 31) * 4);
-      const int slot = slot_of<PAGED>(a, tk, entry, tile);
+    lds_barrier();                        // the last part's reads are done
+    if (tk.len > 0) load_entries(0);
+    // Tiles past the part's last selected key hold nothing (a short row's tail).
+    const int64_t tiles = PAGED ? (tk.len > 0 ? last - first : 0) : selected_tiles(a, tk, first, last, lane);
+    const int mine = __builtin_amdgcn_readfirstlane((int)tiles) - ring;        // this ring's are the i with RINGS i < mine
+    auto queue = [&](int i, uint32_t& mask) {
+      if (L::kAhead > 1) entry = read_lds<int>(own_entries + (uint32_t)(i & 1) * 128 + (lane_here() & 31) * 4);
+      const int slot = slot_of<PAGED>(a, tk, entry, tile_of(i));
       mask = (uint32_t)__ballot(slot >= 0);
-      if (tile + 1 < end) load_entries(tile + 1);
+      if (RINGS * (i + 1) < mine) load_entries(i + 1);
       if (E4M3) {
         const float* at = slot >= 0 ? a.cache.scale + slot : reinterpret_cast<const float*>(kZeroRow);
-        queue_words_to_lds(at, lds_base + L::kScales + (wave * L::kStages + into) * 128);
+        queue_words_to_lds(at, scales + into * 128);
       }
       load_tile<NW, E4M3>(a.cache, slot, lds_base + into * L::kStageBytes, wave);
       into = into + 1 < L::kStages ? into + 1 : 0;
     };
-    if (first < end) {
-      load_entries(first);
-      wait_loads<0>();
-    }
+    wait_loads<0>();                      // the entries
 #pragma unroll
     for (int d = 0; d < L::kAhead; ++d) {
       masks[d] = 0;
-      if (first + d < end) {
-        queue(first + d, masks[d]);
+      if (RINGS * d < mine) {
+        queue(d, masks[d]);
         if (d + 1 < L::kAhead) wait_loads<L::kLoads>();        // the next entries
       }
     }
     int from = 0;                         // the stage of the tile being computed
-    for (int64_t tile = first; tile < end; ++tile) {
-      if (L::kAhead > 1 && tile + 1 < end)
+    for (int i = 0; RINGS * i < mine + ring; ++i) {
+      if (L::kAhead > 1 && RINGS * (i + 1) < mine)
         wait_loads<L::kLoads>();          // all but the next tile's rows
       else
         wait_loads<0>();
       lds_barrier();            // every wave's rows are there, and nobody reads the stage before any more
+      if (RINGS > 1 && RINGS * i >= mine) break;               // (in the last round only)
       masks[L::kAhead] = 0;
-      if (tile + L::kAhead < end) queue(tile + L::kAhead, masks[L::kAhead]);
+      if (RINGS * (i + L::kAhead) < mine) queue(i + L::kAhead, masks[L::kAhead]);
       const uint32_t mask = masks[0];
 #pragma unroll
       for (int d = 0; d < L::kAhead; ++d) masks[d] = masks[d + 1];
-      const uint32_t stage = lds_base + from * L::kStageBytes;
-      const float* sc = scales + from * 32;
+      const uint32_t stage = lds_base + from * L::kStageBytes, sc = scales + from * 128;
       from = from + 1 < L::kStages ? from + 1 : 0;
       f32x4 s[2];
       score_tile<E4M3>(st, s, stage, sc, reads, lane);
       weigh_tile<E4M3>(st, s, stage, sc, mask, scale_log2, reads, lane);
     }
 
+    if (RINGS > 1) {
+      // the second ring's waves hand theirs to the first's
+      f32x4* other_o = reinterpret_cast<f32x4*>(lds + wave * (kHeads * kLatent * 4)) + lane;
+      float2* other_ml = reinterpret_cast<float2*>(lds + NW * (kHeads * kLatent * 4) + wave * 512) + lane;
+      lds_barrier();
+      if (ring > 0) {
+#pragma unroll
+        for (int cb = 0; cb < kColBlocks; ++cb) other_o[cb * 64] = st.o[cb];
+        *other_ml = make_float2(st.m, st.l);
+      }
+      lds_barrier();
+      if (ring == 0) {
+        const float2 ml = *other_ml;
+        const float m = fmaxf(st.m, ml.x);
+        const float f = __builtin_amdgcn_exp2f(st.m - m), g = __builtin_amdgcn_exp2f(ml.x - m);
+        st.m = m;
+        st.l = st.l * f + ml.y * g;
+#pragma unroll
+        for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = st.o[cb] * f + other_o[cb * 64] * g;
+      }
+    }
+    const bool writes = RINGS == 1 || ring == 0;
+
     // this lane's head: its sum is spread over four lanes
     const float l = sum_of_4(st.l);
     if (whole) {
-      if (head < a.num_heads) {
+      if (writes && head < a.num_heads) {
         const float inv = l > 0.f ? 1.0f / l : 0.f;
         const int64_t row = t * a.num_heads + head;
         uint16_t* out = a.out + row * kLatent + 4 * group;
@@ -551,7 +589,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(AttendArgs a) {
       // a part that begins its token is this workgroup's last, any other its first
       const int64_t slot = first == 0 ? a.wgs + share : share;
       const int64_t at = ((int64_t)block * 2 * a.wgs + slot) * NW + wave;
-      if (live_wave) {
+      if (writes && live_wave) {
         float* o = a.part_out + at * (kHeads * kLatent) + lane * 4;
 #pragma unroll
         for (int cb = 0; cb < kColBlocks; ++cb) *reinterpret_cast<f32x4*>(o + cb * 256) = st.o[cb];
@@ -659,18 +697,26 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttendArgs a) {
 
 int ceil_div(int a, int b) { return (int)(((int64_t)a + b - 1) / b); }
 
-template <int NW, bool E4M3>
+template <int NW, int RINGS, bool E4M3>
 hipError_t launch(const AttendArgs& a, hipStream_t stream) {
   const int64_t shares = ceil_div(a.wgs > 0 ? a.wgs : a.num_tokens, 8);
   const int64_t x = shares * 8 * ceil_div(a.num_heads, kHeads * NW);
   if (x > (int64_t)INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)x), block(64 * NW);
-  constexpr int kLds = Lds<NW, E4M3>::kBytes;
+  const dim3 grid((unsigned)x), block(64 * NW * RINGS);
+  constexpr int kLds = Lds<NW, RINGS, E4M3>::kBytes;
   static_assert(sizeof(SplitPlan) <= (size_t)kLds, "the plan is made where the rows go");
-  auto* kernel = a.indices ? attend_kernel<NW, E4M3, false> : attend_kernel<NW, E4M3, true>;
-  hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.wgs == 0) return e;
+  if (a.indices)
+    hipLaunchKernelGGL((attend_kernel<NW, RINGS, E4M3, false>), grid, block, kLds, stream, a);
+  else
+    hipLaunchKernelGGL((attend_kernel<NW, RINGS, E4M3, true>), grid, block, kLds, stream, a);
+  return hipGetLastError();
+}
+
+template <int NW, bool E4M3>
+hipError_t launch(const AttendArgs& a, hipStream_t stream) {
+  if (a.wgs == 0) return launch<NW, 1, E4M3>(a, stream);
+  const hipError_t e = launch<NW, 2, E4M3>(a, stream);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(join_kernel<NW>, dim3((unsigned)a.num_tokens, (unsigned)ceil_div(a.num_heads, kHeads), kColBlocks / kJoinBlocks),
                      dim3(64 * kJoinWaves), 0, stream, a);
   return hipGetLastError();

@@ -91,16 +91,28 @@ float scale_log2(float softmax_scale) {
 }
 
 // Workgroups that share the tiles of a launch of absorbed attention, or 0 for one
-// workgroup per token.
-int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, int32_t num_requests) {
+// workgroup per token.  Not split, two workgroups run on a CU at a time, and the
+// last round of them may leave most CUs idle: split is what leaves more than a
+// third idle (64 heads, 2048 selected bf16 slots, us split and not: 300 tokens
+// 153 and 160, 512 tokens 217 and 203; 700 tokens of 8-bit slots 362 and 339).
+// With 32 heads, split launches are the faster ones throughout (512 tokens 185
+// and 206, 2048 tokens 700 and 728, 8-bit 687 and 789); with 16 they are not
+// (1024 tokens 449 and 427).
+// A workgroup takes kShareTiles tiles or more: one token of 64 tiles x 128 heads
+// took 27.8 us at one tile to a workgroup, 22.3 at two and 21.9 at four; 4 tokens
+// x 64 heads 31.6, 26.6 and 25.3.
+int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, bool paged, int32_t num_requests) {
+  if (paged && (num_tokens > latent::kPlanTokens || num_requests > 65535)) return 0;
   const int heads = latent::attend_heads(num_heads);
   const int64_t blocks = (num_heads + heads - 1) / heads;
-  const int64_t resident = (int64_t)cus * latent::kAttendPerCu;
-  if (num_tokens > latent::kSplitTokens || num_requests > 65535 || num_tokens * blocks >= 4 * resident) return 0;
-  int64_t wgs = resident / blocks;
-  const int64_t tiles = num_tokens * ((keys + latent::kTileKeys - 1) / latent::kTileKeys + 1);
-  if (tiles > (int64_t)INT32_MAX) return 0;   // the plan counts tiles in 32 bits
-  if (wgs > tiles) wgs = tiles;
+  const int64_t token_tiles = (keys + latent::kTileKeys - 1) / latent::kTileKeys + 1;
+  if (token_tiles > (int64_t)INT32_MAX / num_tokens) return 0;   // the plan counts tiles in 32 bits
+  const int64_t items = num_tokens * blocks, round = 2 * (int64_t)cus;
+  const int64_t rounds = (items + round - 1) / round;
+  if (latent::attend_waves(num_heads) != 2 && 3 * items >= 2 * rounds * round) return 0;
+  int64_t wgs = cus / blocks;                                    // one takes a CU's LDS
+  const int64_t most = num_tokens * token_tiles / latent::kShareTiles;
+  if (wgs > most) wgs = most;
   return wgs < 1 ? 1 : (int)wgs;
 }
 
@@ -122,7 +134,7 @@ topk_status_t attend(latent::AttendArgs& a, int64_t keys, bool e4m3, void* works
   int cus = 0;
   const topk_status_t st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
-  a.wgs = split_wgs(cus, a.num_tokens, a.num_heads, keys, a.num_requests);
+  a.wgs = split_wgs(cus, a.num_tokens, a.num_heads, keys, !a.indices, a.num_requests);
   if (a.wgs > 0) {
     const latent::SplitLayout s = latent::split_layout(a.num_tokens, a.num_heads, a.wgs);
     if (!workspace || workspace_bytes < s.total()) return invalid("the workspace is smaller than latent_attention_workspace says");
@@ -282,7 +294,7 @@ topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, 
   int cus = 0;
   const topk_status_t st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
-  const int wgs = split_wgs(cus, num_tokens, num_heads, keys, 0);
+  const int wgs = split_wgs(cus, num_tokens, num_heads, keys, false, 0);   // the same for whole sequences, or 0
   if (wgs > 0) *bytes = latent::split_layout(num_tokens, num_heads, wgs).total();
   return TOPK_SUCCESS;
 }

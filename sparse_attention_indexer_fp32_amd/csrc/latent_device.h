@@ -43,7 +43,8 @@ __device__ __forceinline__ int acc_row(int r, int hb) { return 8 * (r >> 2) + 4 
 //   * transposed, 32 lanes at a time: a chunk pair of 8 rows, or two neighbouring pairs of
 //     4 rows, so rows differ in the pair's number, bits 0 and 1 of the row in
 //     its upper two bits.
-// Both hold for this linear map.  (A map that missed the second lost half of all LDS
+// Both hold for this linear map (and for rotary rows, 8 chunks and two rows to 256
+// bytes, with chunk ^ row / 2).  (A map that missed the second lost half of all LDS
 // cycles to conflicts, one that missed the first a quarter.)
 __device__ __forceinline__ int swizzle(int row) {
   return ((row & 3) << 2) ^ ((row >> 1) & 2) ^ ((row >> 3) & 1) * 3;

@@ -83,7 +83,8 @@ hipError_t launch_cache_load(const LoadArgs& a, bool e4m3, hipStream_t stream);
 // whole ones and begin another; parts of a token go to the workspace and are
 // joined by a second launch.  Not split: one workgroup per token.
 constexpr int kTileKeys = 32;
-constexpr int kSplitTokens = 1024;   // tokens a split launch takes at most
+constexpr int kShareTiles = 4;       // tiles a workgroup of a split launch takes at least
+constexpr int kPlanTokens = 1024;    // tokens a split launch over whole sequences takes at most
 
 struct AttendArgs {
   const uint16_t* q;
@@ -109,9 +110,8 @@ struct AttendArgs {
   int32_t* part_rec;
 };
 
-// Workgroups a CU holds; by head count, the waves of a workgroup and the heads it
-// takes; and the workspace of a split launch.
-constexpr int kAttendPerCu = 2;
+// By head count: waves that share a ring of tiles, and heads they take; and the
+// workspace of a split launch.
 int attend_waves(int num_heads);
 int attend_heads(int num_heads);
 struct SplitLayout {

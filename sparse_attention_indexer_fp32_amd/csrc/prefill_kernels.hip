@@ -35,6 +35,7 @@ constexpr int kRopeBytes = kRope * 2;
 constexpr int kHeadSteps = kHead / 16;       // 8 steps of the first product
 constexpr int kRopeSteps = kRope / 16;       // and 4 of the rotary part
 constexpr int kColBlocks = kHead / 32;       // 4 blocks of O^T
+constexpr int kReadsAhead = 4;               // LDS reads in flight before a matrix instruction
 
 struct Stage {
   char up[kKeys * kUpBytes];
@@ -107,7 +108,7 @@ __device__ __forceinline__ TileLoads tile_loads(const PrefillArgs& a, int rows, 
   for (int i = 0; i < kKeys / 8 / kWaves; ++i) {
     const int key = 8 * (wave * (kKeys / 8 / kWaves) + i) + (lane >> 3);
     const int row = key < rows ? key : rows - 1;
-    t.rope[i] = (uint32_t)row * (uint32_t)(a.rope_stride * 2) + (uint32_t)(((lane ^ key) & 7) * 16);
+    t.rope[i] = (uint32_t)row * (uint32_t)(a.rope_stride * 2) + (uint32_t)(((lane ^ (key >> 1)) & 7) * 16);
   }
   return t;
 }
@@ -129,24 +130,22 @@ struct RowState {
   float l;      // this lane's part of the sum
 };
 
-// A lane's LDS offsets within a tile.
+// A lane's LDS offsets within a tile.  The other offsets differ from these in
+// bits that the swizzle only flips (chunk 2 k + hb in bits 5 to 7, column block
+// in bits 6 and 7), and are formed where they are read.
 struct TileReads {
-  uint32_t key[kHeadSteps];            // of row lane % 32, 16-byte chunk 2 k + hb
-  uint32_t rope[kRopeSteps];
-  uint32_t value[kColBlocks];          // transposed reads of rows 4 hb + 0..3, column block cb
+  int key;      // row lane % 32, chunk hb
+  int rope;
+  int value;    // transposed reads of rows 4 hb + 0..3, column block 0
 };
 
 __device__ __forceinline__ TileReads tile_reads(int lane) {
-  TileReads t;
   const int i = lane & 31, hb = lane >> 5, j = lane & 15, quarter = (lane >> 4) & 1;
-#pragma unroll
-  for (int k = 0; k < kHeadSteps; ++k) t.key[k] = i * kUpBytes + (((2 * k + hb) ^ swizzle(i)) << 4);
-#pragma unroll
-  for (int k = 0; k < kRopeSteps; ++k) t.rope[k] = i * kRopeBytes + ((((2 * k + hb) ^ i) & 7) << 4);
   const int key = 4 * hb + (j >> 2);
-#pragma unroll
-  for (int cb = 0; cb < kColBlocks; ++cb)
-    t.value[cb] = key * kUpBytes + kUpBytes / 2 + (((cb * 4 + 2 * quarter + ((j & 3) >> 1)) ^ swizzle(key)) << 4) + (j & 1) * 8;
+  TileReads t;
+  t.key = i * kUpBytes + ((hb ^ swizzle(i)) << 4);
+  t.rope = i * kRopeBytes + (((hb ^ (i >> 1)) & 7) << 4);
+  t.value = key * kUpBytes + kUpBytes / 2 + (((2 * quarter + ((j & 3) >> 1)) ^ swizzle(key)) << 4) + (j & 1) * 8;
   return t;
 }
 
@@ -200,16 +199,16 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
                                             float scale_log2, int lane) {
   const int hb = lane >> 5;
   const uint32_t stage = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)t.up;
-  f32x16 s[2];
-#pragma unroll
-  for (int kb = 0; kb < 2; ++kb) {
-    s[kb] = f32x16{};
-#pragma unroll
-    for (int k = 0; k < kHeadSteps; ++k)
-      s[kb] = mfma(*reinterpret_cast<const bf16x8*>(t.up + 32 * kb * kUpBytes + at.key[k]), st.q[k], s[kb]);
-#pragma unroll
-    for (int k = 0; k < kRopeSteps; ++k)
-      s[kb] = mfma(*reinterpret_cast<const bf16x8*>(t.rope + 32 * kb * kRopeBytes + at.rope[k]), st.q[kHeadSteps + k], s[kb]);
+  f32x16 s[2] = {f32x16{}, f32x16{}};
+  {
+    const uint32_t key = (uint32_t)here(at.key + (int)stage), rope = (uint32_t)here(at.rope + (int)stage) + kKeys * kUpBytes;
+    run_ahead<2 * (kHeadSteps + kRopeSteps), kReadsAhead>(
+        [&](int n) {
+          const int k = n >> 1, kb = n & 1;
+          return read_lds<bf16x8>(k < kHeadSteps ? (key ^ (uint32_t)(k << 5)) + 32 * kb * kUpBytes
+                                                 : (rope ^ (uint32_t)((k - kHeadSteps) << 5)) + 32 * kb * kRopeBytes);
+        },
+        [&](int n, bf16x8 rows) { s[n & 1] = mfma(rows, st.q[n >> 1], s[n & 1]); });
   }
   float top = -INFINITY;
   const int own_limit = limit - 4 * hb;
@@ -247,18 +246,19 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
     add_values_one_by_one(st.o, s, t, limit, here(lane));
     return;
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int cb = 0; cb < kColBlocks; ++cb) {
-      // step k: rows 32 (k / 2) + 8 (k % 2) + 4 hb + 0..3 and those 16 on; rows 8 on swizzle with bits 0 and 1 flipped
-      const uint32_t v = stage + 32 * (k >> 1) * kUpBytes + 8 * (k & 1) * kUpBytes + (at.value[cb] ^ (uint32_t)((k & 1) * 48));
-      st.o[cb] = mfma(join8(read_tr(v), read_tr(v + 16 * kUpBytes)), p[k], st.o[cb]);
-    }
+  const uint32_t value = (uint32_t)here(at.value + (int)stage);
+  run_ahead<4 * kColBlocks, kReadsAhead>(
+      [&](int n) {
+        // step k: rows 32 (k / 2) + 8 (k % 2) + 4 hb + 0..3 and those 16 on; rows 8 on swizzle with bits 0 and 1 flipped
+        const int k = n / kColBlocks, cb = n % kColBlocks;
+        const uint32_t v = (value ^ (uint32_t)((cb << 6) ^ (k & 1) * 48)) + (32 * (k >> 1) + 8 * (k & 1)) * kUpBytes;
+        return join8(read_tr(v), read_tr(v + 16 * kUpBytes));
+      },
+      [&](int n, bf16x8 cols) { st.o[n % kColBlocks] = mfma(cols, p[n / kColBlocks], st.o[n % kColBlocks]); });
 }
 
 __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, int64_t blocks) {
-  __shared__ __attribute__((aligned(16))) Stage stage0, stage1;
+  __shared__ __attribute__((aligned(256))) Stage stage0, stage1;
   const int lane = threadIdx.x & 63, hb = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Heads in turn, and of a head its last (longest) blocks first; each XCD
