@@ -206,7 +206,8 @@ topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, 
  *   q        (num_tokens, num_heads, LATENT_HEAD_DIM + LATENT_ROPE_DIM) bf16,
  *            token and head strides in elements.
  *   kv_up    (num_kv, num_heads, 2 * LATENT_HEAD_DIM) bf16, token and head
- *            strides: each head's key (without the rotary part), then its value.
+ *            strides: each head's key (without the rotary part), then its
+ *            value.  Token strides (rope's too) are below 2^24 elements.
  *   rope     (num_kv, LATENT_ROPE_DIM) bf16, row stride: the rotary keys,
  *            shared by the heads.
  *   q_starts, kv_starts   (num_requests + 1,) int32, ascending from 0:
@@ -218,14 +219,19 @@ topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, 
  *            num_heads) fp32 or NULL: as latent_attention.
  * A query with no key gets zeros and -inf.  Rows of q from
  * q_starts[num_requests] on are left as they are in out and lse; key rows from
- * kv_starts[num_requests] on are not read.
+ * kv_starts[num_requests] on are not read.  The workspace is
+ * latent_attention_expanded_workspace's, otherwise as latent_attention's.
  */
 topk_status_t latent_attention_expanded(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
                                         const uint16_t* kv_up, int64_t kv_token_stride, int64_t kv_head_stride,
                                         const uint16_t* rope, int64_t rope_stride, const int32_t* q_starts,
                                         const int32_t* kv_starts, float softmax_scale, int32_t causal, uint16_t* out,
-                                        float* lse, hipStream_t stream, int32_t num_tokens, int64_t num_kv,
-                                        int32_t num_heads, int32_t num_requests);
+                                        float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                                        int32_t num_tokens, int64_t num_kv, int32_t num_heads, int32_t num_requests);
+
+/* Bytes of workspace of a call with these sizes (on the current device). */
+topk_status_t latent_attention_expanded_workspace(int32_t num_tokens, int32_t num_heads, int64_t num_kv,
+                                                  int32_t num_requests, size_t* bytes);
 
 #ifdef __cplusplus
 }

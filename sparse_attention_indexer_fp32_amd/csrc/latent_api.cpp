@@ -84,6 +84,9 @@ topk_status_t check_cache(const void* latent, int64_t latent_stride, const uint1
   return TOPK_SUCCESS;
 }
 
+// Largest row stride (elements) of the expanded form's keys: byte offsets within a tile of 64 rows take 32 bits.
+constexpr int64_t kMaxTileStride = (1 << 24) - 8;
+
 // The kernels' scale: in log2 units, and not quite 0, which would make 0 * -inf
 // of a masked score (2^-100 leaves every score as good as 0).
 float scale_log2(float softmax_scale) {
@@ -114,6 +117,20 @@ int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, bool
   const int64_t most = num_tokens * token_tiles / latent::kShareTiles;
   if (wgs > most) wgs = most;
   return wgs < 1 ? 1 : (int)wgs;
+}
+
+// The same for the expanded form: workgroups that share all units' tiles, or 0
+// for one workgroup per unit (at most two run on a CU at a time).  Split pays
+// where units leave a quarter of the card idle and are long, 32 tiles of 64
+// keys on average (us split and not, new tokens x heads behind cached
+// ones: 100 x 8 behind 60000 92 and 1335; 2048 x 16 behind 2048 99 and 112; 128
+// x 64 behind 2000 57 and 66, behind 1000 54 and 43; 1500 x 32 behind 6000 266
+// and 266, 2048 x 32 behind 8000 427 and 390: shares of a head read
+// different keys at a time, blocks of a head the same ones out of L2).
+int prefill_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t num_kv, int32_t num_requests) {
+  const int64_t units = latent::prefill_blocks(num_tokens, num_requests) * num_heads, round = 2 * (int64_t)cus;
+  const bool pays = 4 * units < 3 * round && num_kv >= 32 * 64 * (int64_t)num_requests;
+  return num_requests <= latent::kPlanRequests && pays ? (int)round : 0;
 }
 
 topk_status_t check_queries(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const uint16_t* out,
@@ -365,12 +382,28 @@ topk_status_t latent_attention_paged(const uint16_t* q, int64_t q_token_stride, 
                 stream);
 }
 
+topk_status_t latent_attention_expanded_workspace(int32_t num_tokens, int32_t num_heads, int64_t num_kv,
+                                                  int32_t num_requests, size_t* bytes) {
+  topk::set_last_error("");
+  if (!bytes) return invalid("bytes must be non-null");
+  if (num_tokens < 0 || num_heads < 0 || num_kv < 0 || num_requests < 0)
+    return invalid("num_tokens, num_heads, num_kv and num_requests must be >= 0");
+  *bytes = 0;
+  if (num_tokens == 0 || num_heads == 0 || num_requests == 0) return TOPK_SUCCESS;
+  int cus = 0;
+  const topk_status_t st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  const int wgs = prefill_wgs(cus, num_tokens, num_heads, num_kv, num_requests);
+  if (wgs > 0) *bytes = latent::prefill_split_layout(num_tokens, num_heads, num_requests, wgs).total();
+  return TOPK_SUCCESS;
+}
+
 topk_status_t latent_attention_expanded(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
                                         const uint16_t* kv_up, int64_t kv_token_stride, int64_t kv_head_stride,
                                         const uint16_t* rope, int64_t rope_stride, const int32_t* q_starts,
                                         const int32_t* kv_starts, float softmax_scale, int32_t causal, uint16_t* out,
-                                        float* lse, hipStream_t stream, int32_t num_tokens, int64_t num_kv,
-                                        int32_t num_heads, int32_t num_requests) {
+                                        float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                                        int32_t num_tokens, int64_t num_kv, int32_t num_heads, int32_t num_requests) {
   topk::set_last_error("");
   topk_status_t st =
       check_queries(q, q_token_stride, q_head_stride, out, num_tokens, num_heads, LATENT_HEAD_DIM + LATENT_ROPE_DIM);
@@ -384,6 +417,8 @@ topk_status_t latent_attention_expanded(const uint16_t* q, int64_t q_token_strid
   if (kv_token_stride < 0 || kv_head_stride < 0 || (num_heads > 1 && kv_head_stride < 2 * LATENT_HEAD_DIM) ||
       rope_stride < LATENT_ROPE_DIM)
     return invalid("kv_up's heads or rope's rows overlap, or a stride is negative");
+  if (kv_token_stride > kMaxTileStride || rope_stride > kMaxTileStride)
+    return invalid("kv_up's and rope's rows must be less than 2^24 elements apart");
   if (!aligned(kv_up) || !aligned(rope) || kv_token_stride % 8 != 0 || kv_head_stride % 8 != 0 || rope_stride % 8 != 0)
     return invalid("kv_up's and rope's rows must start on 16-byte boundaries");
   int cus = 0;
@@ -408,7 +443,20 @@ topk_status_t latent_attention_expanded(const uint16_t* q, int64_t q_token_strid
   a.num_kv = num_kv;
   a.num_heads = num_heads;
   a.num_requests = num_requests;
-  return launched(latent::launch_prefill(a, stream), "latent-attention-expanded");
+  a.wgs = prefill_wgs(cus, num_tokens, num_heads, num_kv, num_requests);
+  if (a.wgs > 0) {
+    const latent::SplitLayout s = latent::prefill_split_layout(num_tokens, num_heads, num_requests, a.wgs);
+    if (!workspace || workspace_bytes < s.total())
+      return invalid("the workspace is smaller than latent_attention_expanded_workspace says");
+    if (!aligned(workspace)) return invalid("the workspace must start on a 16-byte boundary");
+    char* p = static_cast<char*>(workspace);
+    a.part_out = reinterpret_cast<float*>(p);
+    a.part_ml = reinterpret_cast<float2*>(p + s.out_bytes);
+    a.part_rec = reinterpret_cast<int32_t*>(p + s.out_bytes + s.ml_bytes);
+  }
+  char buf[96];
+  std::snprintf(buf, sizeof(buf), "latent-attention expanded wgs=%d", a.wgs);
+  return launched(latent::launch_prefill(a, stream), buf);
 }
 
 }  // extern "C"

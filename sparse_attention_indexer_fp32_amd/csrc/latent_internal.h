@@ -122,6 +122,10 @@ SplitLayout split_layout(int num_tokens, int num_heads, int wgs);
 hipError_t launch_attend(const AttendArgs& a, bool e4m3, hipStream_t stream);
 
 // Expanded form.
+// Expanded form.  A unit is a block of 128 queries of one head.  Split: `wgs`
+// workgroups share all units' tiles of 64 keys evenly, as above.
+constexpr int kPlanRequests = 512;       // requests a split launch takes at most
+constexpr int kPrefillShareTiles = 8;    // tiles a workgroup of a split launch takes at least
 struct PrefillArgs {
   const uint16_t* q;
   int64_t q_token_stride, q_head_stride;   // elements
@@ -139,7 +143,13 @@ struct PrefillArgs {
   int64_t num_kv;
   int32_t num_heads;
   int32_t num_requests;
+  int32_t wgs;               // split: workgroups; 0: one per unit
+  float* part_out;           // workspace of a split launch (prefill_split_layout)
+  float2* part_ml;
+  int32_t* part_rec;
 };
+int64_t prefill_blocks(int num_tokens, int num_requests);   // of one head, at most
+SplitLayout prefill_split_layout(int num_tokens, int num_heads, int num_requests, int wgs);
 hipError_t launch_prefill(const PrefillArgs& a, hipStream_t stream);
 
 }  // namespace latent

@@ -21,7 +21,7 @@ _BF16, _E4M3 = 0, 1
 
 EXPORTED_LATENT = ("paged_append_plan", "latent_cache_store", "latent_cache_load", "latent_cache_load_paged",
                    "latent_attention", "latent_attention_paged", "latent_attention_workspace",
-                   "latent_attention_expanded")
+                   "latent_attention_expanded", "latent_attention_expanded_workspace")
 
 
 class AppendPlan(NamedTuple):
@@ -46,8 +46,9 @@ def declare(lib: ctypes.CDLL) -> None:
         "latent_attention_paged": [vp, i64, i64] + cache + [vp, vp, vp, i32, f32, vp, vp, vp, size, vp, i32, i32, i32,
                                                             i64, i64],
         "latent_attention_workspace": [i32, i32, i64, ctypes.POINTER(size)],
-        "latent_attention_expanded": [vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, f32, i32, vp, vp, vp, i32, i64, i32,
-                                      i32],
+        "latent_attention_expanded": [vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, f32, i32, vp, vp, vp, size, vp, i32,
+                                      i64, i32, i32],
+        "latent_attention_expanded_workspace": [i32, i32, i64, i32, ctypes.POINTER(size)],
     }
     for name, args in types.items():
         fn = getattr(lib, name)
@@ -156,15 +157,15 @@ def _made(out, lse, tokens: int, heads: int, width: int, dev):
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_bytes(device_index: int, tokens: int, heads: int, keys: int) -> int:
+def _workspace_bytes(device_index: int, query: str, *sizes: int) -> int:
     n = ctypes.c_size_t(0)
-    package._check(package.load().latent_attention_workspace(tokens, heads, keys, ctypes.byref(n)))
+    package._check(getattr(package.load(), query)(*sizes, ctypes.byref(n)))
     return n.value
 
 
-def _workspace(dev, tokens: int, heads: int, keys: int):
+def _workspace(dev, query: str, *sizes: int):
     """The workspace of a call as (tensor to hold on to, pointer, bytes)."""
-    n = _workspace_bytes(dev.index, tokens, heads, keys)
+    n = _workspace_bytes(dev.index, query, *sizes)
     if n == 0:
         return None, None, 0
     w = torch.empty(n, dtype=torch.uint8, device=dev)
@@ -335,7 +336,7 @@ def latent_attention(q, latent, rope, indices, softmax_scale: float, scale=None,
 
     def args(handle):
         got.extend(_made(out, lse, T, H, LATENT_DIM, dev))
-        got.extend(_workspace(dev, T, H, k))
+        got.extend(_workspace(dev, "latent_attention_workspace", T, H, k))
         return (*qargs, *cache, indices.data_ptr(), float(softmax_scale), got[0].data_ptr(), got[1].data_ptr(), got[3],
                 got[4], handle, T, H, k, slots)
 
@@ -367,7 +368,7 @@ def latent_attention_paged(q, latent, rope, page_table, seq_lens, q_starts, page
 
     def args(handle):
         got.extend(_made(out, lse, T, H, LATENT_DIM, dev))
-        got.extend(_workspace(dev, T, H, P * int(page_size)))
+        got.extend(_workspace(dev, "latent_attention_workspace", T, H, P * int(page_size)))
         return (*qargs, *cache, page_table.data_ptr(), seq_lens.data_ptr(), q_starts.data_ptr(), int(page_size),
                 float(softmax_scale), got[0].data_ptr(), got[1].data_ptr(), got[3], got[4], handle, T, H, B, P, slots)
 
@@ -405,10 +406,12 @@ def latent_attention_expanded(q, kv_up, rope, q_starts, kv_starts, softmax_scale
 
     def args(handle):
         got.extend(_made(out, lse, T, H, LATENT_HEAD_DIM, dev))
+        got.extend(_workspace(dev, "latent_attention_expanded_workspace", T, H, K, B))
         return (*qargs, kv_up.data_ptr(), kv_up.stride(0) if K > 1 else H * 2 * LATENT_HEAD_DIM,
                 kv_up.stride(1) if H > 1 else 2 * LATENT_HEAD_DIM, rope.data_ptr(),
                 rope.stride(0) if K > 1 else LATENT_ROPE_DIM, q_starts.data_ptr(), kv_starts.data_ptr(),
-                float(softmax_scale), int(bool(causal)), got[0].data_ptr(), got[1].data_ptr(), handle, T, K, H, B)
+                float(softmax_scale), int(bool(causal)), got[0].data_ptr(), got[1].data_ptr(), *got[3:5],
+                handle, T, K, H, B)
 
     _call("latent_attention_expanded", dev, stream, args)
     return got[0], got[1]

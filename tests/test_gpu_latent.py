@@ -266,7 +266,7 @@ def test_load_paged(lib, dev, e4m3, lens):
 SELECTED = [
     # tokens, heads, k
     (1, 1, 1), (1, 32, 33), (2, 5, 64), (3, 33, 200), (1, 64, 2048), (5, 128, 100), (2, 70, 97), (4, 130, 65),
-    (40, 8, 512), (300, 3, 40), (1100, 2, 31), (2, 16, 0),
+    (40, 8, 512), (300, 3, 40), (1100, 2, 31), (2, 16, 0), (350, 50, 70), (60, 24, 300),
 ]
 
 
@@ -347,6 +347,9 @@ PAGED = {
     "heads_128": ([150, 90], [2, 1], 128, 64, 1),
     "many": (list(range(1, 1150)), [1] * 1149, 2, 16, 0),     # more tokens than a split launch takes
     "one_prompt": ([700], [700], 2, 16, 5),
+    "wide_many": ([1 + i % 67 for i in range(1030)], [1] * 1030, 20, 16, 0),
+    "wide_64": ([3 + i % 90 for i in range(360)], [1] * 360, 50, 16, 1),
+    "wide_prompts": ([300, 40, 100], [200, 0, 90], 24, 64, 4),
 }
 
 
@@ -376,7 +379,7 @@ def test_paged(lib, dev, e4m3, name):
     out, lse = _host(out), _host(lse)
     assert (out[starts[-1]:] == GUARD).all() and (lse[starts[-1]:] == GUARD).all()
     heads = None if H <= 12 else [0, H // 2, H - 1]
-    for b in range(B) if B < 100 else (0, 1, 700, B - 1):
+    for b in range(B) if B < 100 else (0, 1, 700 % B, B - 1):
         for i in range(new[b]) if new[b] < 100 else (0, 1, 33, new[b] - 1):
             n = lo.causal_keys(i, new[b], lens[b])
             s = lo.page_slots(table[b], ps, n, cache.slots)
@@ -396,6 +399,11 @@ EXPANDED = {
     "single_tokens": ([1] * 70, list(range(1, 71)), 2, True, 1),
     "tiles": ([257], [1000], 9, True, 0),
     "long": ([700], [1500], 2, True, 0),
+    # long key ranges and few queries: blocks are shared by several workgroups
+    "tiles_split": ([1, 130, 0, 70, 5], [9000, 4000, 3000, 64, 2], 3, True, 2),
+    "tiles_split_chunk": ([1000], [4100], 2, True, 0),
+    "tiles_split_not_causal": ([33, 200], [5000, 1000], 2, False, 0),
+    "tiles_split_one": ([1], [20001], 1, True, 0),
 }
 
 
@@ -431,6 +439,49 @@ def test_expanded(lib, dev, name):
                 for err in (lo.check(f"{b} {i} {h} out", out[qs[b] + i, h], a.out, a.out_bound),
                             lo.check(f"{b} {i} {h} lse", lse[qs[b] + i, h], a.lse, a.lse_bound)):
                     assert err is None, err
+
+
+def test_expanded_split_over_many_requests(lib, dev):
+    """300 requests of one query and 2000 to 2200 keys; one key row (stride 0)
+    serves all, so weights come from the rotary part."""
+    import torch
+    rng = np.random.default_rng(61)
+    B = 300
+    nk = 2000 + rng.integers(0, 200, B)
+    nk[7], nk[8] = 0, 3000
+    ks = np.concatenate([[0], np.cumsum(nk)])
+    K = int(ks[-1])
+    assert K >= 2048 * B
+    q, qh = _bf(rng, (B, 1, 192), dev)
+    row, rowh = _bf(rng, (1, 1, 256), dev)
+    rope, rh = _bf(rng, (K, 64), dev)
+    out, lse = lib.latent_attention_expanded(q, row.expand(K, 1, 256), rope, _i32(range(B + 1), dev), _i32(ks, dev), 0.2)
+    out, lse = _host(out), _host(lse)
+    for b in list(range(0, B, 23)) + [7, 8, B - 1]:
+        n = int(nk[b])
+        keys = np.concatenate([np.repeat(rowh[0, :, :128], n, 0), rh[ks[b]:ks[b] + n]], 1)
+        a = lo.attend(qh[b, 0], keys, np.repeat(rowh[0, :, 128:], n, 0), 0.2)
+        for err in (lo.check(f"{b} out", out[b, 0], a.out, a.out_bound), lo.check(f"{b} lse", lse[b, 0], a.lse, a.lse_bound)):
+            assert err is None, err
+
+
+def test_expanded_small_workspace_is_refused(lib, dev):
+    import ctypes
+
+    import torch
+    n = ctypes.c_size_t(0)
+    handle = lib.load()
+    assert handle.latent_attention_expanded_workspace(1, 2, 9000, 1, ctypes.byref(n)) == 0 and n.value > 0
+    x = torch.zeros((9000, 2, 256), dtype=torch.bfloat16, device=dev)
+    starts, ends = _i32([0, 1], dev), _i32([0, 9000], dev)
+    out = torch.full((1, 2, 128), float(GUARD), dtype=torch.bfloat16, device=dev)
+    ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    for w, b in ((None, 0), (ws.data_ptr(), n.value - 1), (ws.data_ptr() + 8, n.value)):
+        assert handle.latent_attention_expanded(x.data_ptr(), 384, 192, x.data_ptr(), 512, 256, x.data_ptr(), 64,
+                                                starts.data_ptr(), ends.data_ptr(), 0.1, 1, out.data_ptr(), None, w, b,
+                                                torch.cuda.current_stream().cuda_stream, 1, 9000, 2, 1) == 1
+    torch.cuda.synchronize()
+    assert (out == GUARD).all()
 
 
 def test_expanded_not_finite_where_masked(lib, dev):

@@ -197,17 +197,18 @@ def test_paged_refusals(lib, kw):
 
 def _expanded(lib, **kw):
     a = dict(q=A, qts=4 * 192, qhs=192, kv=A, kts=4 * 256, khs=256, rope=A, rs=64, qst=A, kst=A, out=A, lse=A, T=5, K=7,
-             H=4, B=2)
+             H=4, B=2, ws=None, wsb=0)
     a.update(kw)
     return lib.latent_attention_expanded(a["q"], a["qts"], a["qhs"], a["kv"], a["kts"], a["khs"], a["rope"], a["rs"],
-                                         a["qst"], a["kst"], 0.1, 1, a["out"], a["lse"], None, a["T"], a["K"], a["H"],
-                                         a["B"])
+                                         a["qst"], a["kst"], 0.1, 1, a["out"], a["lse"], a["ws"], a["wsb"], None, a["T"],
+                                         a["K"], a["H"], a["B"])
 
 
 @pytest.mark.parametrize("kw", [dict(q=None), dict(q=A + 2), dict(qhs=180), dict(qhs=196), dict(qts=-8), dict(kv=None),
                                 dict(kv=A + 8), dict(khs=250), dict(khs=260), dict(kts=4), dict(rope=None),
                                 dict(rope=A + 8), dict(rs=60), dict(rs=68), dict(qst=None), dict(kst=None),
-                                dict(out=None), dict(T=-1), dict(K=-1), dict(H=-1), dict(H=70000), dict(B=-1)])
+                                dict(out=None), dict(T=-1), dict(K=-1), dict(H=-1), dict(H=70000), dict(B=-1),
+                                dict(kts=1 << 24), dict(rs=1 << 24)])
 def test_expanded_refusals(lib, kw):
     assert _expanded(lib, **kw) == 1 and topk.topk_last_error()
 
@@ -220,6 +221,11 @@ def test_nothing_to_do_is_no_error(lib):
     assert lib.latent_attention_workspace(0, 8, 100, ctypes.byref(n)) == 0 and n.value == 0
     assert lib.latent_attention_workspace(-1, 8, 100, ctypes.byref(n)) == 1
     assert lib.latent_attention_workspace(1, 8, 100, None) == 1
+    n.value = 5
+    assert lib.latent_attention_expanded_workspace(0, 8, 100, 2, ctypes.byref(n)) == 0 and n.value == 0
+    for bad in [(-1, 8, 100, 2), (3, -1, 100, 2), (3, 8, -1, 2), (3, 8, 100, -1)]:
+        assert lib.latent_attention_expanded_workspace(*bad, ctypes.byref(n)) == 1
+    assert lib.latent_attention_expanded_workspace(3, 8, 100, 2, None) == 1
 
 
 def test_binding_refuses_before_any_call():
