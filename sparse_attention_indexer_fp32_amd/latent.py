@@ -57,15 +57,20 @@ def declare(lib: ctypes.CDLL) -> None:
 
 
 package = torch = None   # this package and torch, once a call has needed them
+_INT32 = _BFLOAT16 = _FLOAT32 = _UINT8 = _current_device = None
 
 
 def _modules() -> None:
-    """Binds both names above (they are not imported with this module: the
+    """Binds the names above (they are not imported with this module: the
     package loads without torch, and imports this module)."""
-    global package, torch
+    global package, torch, _INT32, _BFLOAT16, _FLOAT32, _UINT8, _current_device
     import torch as torch_module
 
     import sparse_attention_indexer_fp32_amd as this_package
+    _INT32, _BFLOAT16 = torch_module.int32, torch_module.bfloat16
+    _FLOAT32, _UINT8 = torch_module.float32, torch_module.uint8
+    # without the check that CUDA is initialised: a tensor is on the device already
+    _current_device = getattr(torch_module._C, "_cuda_getDevice", torch_module.cuda.current_device)
     torch, package = torch_module, this_package
 
 
@@ -84,75 +89,81 @@ def _call(name: str, dev, stream, make_args):
     """Calls an entry point on its device; make_args(stream handle) gives its
     arguments and allocates what the caller did not pass."""
     fn = getattr(package.load(), name)
-    if stream is None and dev.index == torch.cuda.current_device():
+    if stream is None and dev.index == _current_device():
         st = fn(*make_args(package._stream_handle(None, dev)))
     else:
         with _on(dev, stream):
             st = fn(*make_args(package._stream_handle(stream, dev)))
-    package._check(st)
+    if st:
+        package._check(st)
 
 
-def _int32(name: str, t, shape, dev) -> None:
-    if not (t.dtype == torch.int32 and tuple(t.shape) == shape and t.is_contiguous() and t.device == dev):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}")
+# The checks below run before every launch, and launches here take
+# microseconds: they read each property of a tensor once (a tenth of a
+# microsecond each), and compare device numbers rather than devices.
+
+def _is(t, dtype, shape, at: int) -> bool:
+    """Whether t is a contiguous tensor of this type and shape on device `at`."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == at
+
+
+def _int32(name: str, t, shape, at: int) -> None:
+    if not (t.dtype is _INT32 and t.shape == shape and t.is_contiguous() and t.get_device() == at):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on device {at}")
 
 
 def _gpu(t, name: str):
+    """t's device, and its number."""
     if torch is None:
         _modules()
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
-    return t.device
+    return t.device, t.get_device()
 
 
-def _cache(latent, rope, scale, dev):
+def _cache(latent, rope, scale, at: int):
     """The cache arguments of a call, and the number of slots."""
-    if not (latent.dim() == 2 and latent.shape[1] == LATENT_DIM and latent.stride(1) == 1 and latent.device == dev):
-        raise ValueError(f"latent must be a (slots, {LATENT_DIM}) tensor with contiguous rows on {dev}")
-    slots = latent.shape[0]
-    if not (rope.dim() == 2 and tuple(rope.shape) == (slots, LATENT_ROPE_DIM) and rope.dtype == torch.bfloat16
-          and rope.stride(1) == 1 and rope.device == dev):
+    shape, strides = latent.shape, latent.stride()
+    if not (len(shape) == 2 and shape[1] == LATENT_DIM and strides[1] == 1 and latent.get_device() == at):
+        raise ValueError(f"latent must be a (slots, {LATENT_DIM}) tensor with contiguous rows on device {at}")
+    slots, rope_strides = shape[0], rope.stride()
+    if not (rope.shape == (slots, LATENT_ROPE_DIM) and rope.dtype is _BFLOAT16 and rope_strides[1] == 1
+            and rope.get_device() == at):
         raise ValueError(f"rope must be a (slots, {LATENT_ROPE_DIM}) bfloat16 tensor with contiguous rows on latent's device")
     if scale is None:
-        if latent.dtype != torch.bfloat16:
+        if latent.dtype is not _BFLOAT16:
             raise ValueError("latent must be bfloat16, or uint8 (fp8 E4M3 codes) with scale")
         kind, sp = _BF16, None
     else:
-        if not (latent.dtype == torch.uint8 and scale.dtype == torch.float32 and tuple(scale.shape) == (slots,)
-              and scale.is_contiguous() and scale.device == dev):
+        if not (latent.dtype is _UINT8 and _is(scale, _FLOAT32, (slots,), at)):
             raise ValueError("an 8-bit cache is latent uint8 (fp8 E4M3 codes) and scale, a contiguous (slots,) float32 tensor on its device")
         kind, sp = _E4M3, scale.data_ptr()
     # a single row has no stride to speak of
-    ls = latent.stride(0) if slots > 1 else LATENT_DIM
-    rs = rope.stride(0) if slots > 1 else LATENT_ROPE_DIM
+    ls, rs = (strides[0], rope_strides[0]) if slots > 1 else (LATENT_DIM, LATENT_ROPE_DIM)
     return (latent.data_ptr(), ls, rope.data_ptr(), rs, sp, kind), slots
 
 
 def _queries(q, width: int):
-    if not (q.dim() == 3 and q.shape[2] == width and q.dtype == torch.bfloat16 and (q.stride(2) == 1 or q.numel() == 0)):
+    shape, strides = q.shape, q.stride()
+    if not (len(shape) == 3 and shape[2] == width and q.dtype is _BFLOAT16 and (strides[2] == 1 or q.numel() == 0)):
         raise ValueError(f"q must be a (tokens, heads, {width}) bfloat16 tensor whose last dimension is contiguous")
-    tokens, heads = q.shape[0], q.shape[1]
-    return tokens, heads, (q.data_ptr(), q.stride(0) if tokens > 1 else heads * width,
-                           q.stride(1) if heads > 1 else width)
+    tokens, heads = shape[0], shape[1]
+    return tokens, heads, (q.data_ptr(), strides[0] if tokens > 1 else heads * width, strides[1] if heads > 1 else width)
 
 
-def _outputs(out, lse, tokens: int, heads: int, width: int, dev):
+def _outputs(out, lse, tokens: int, heads: int, width: int, at: int):
     """Checks the outputs that are passed; those that are not are made by _made."""
-    if out is not None:
-        if not (out.dtype == torch.bfloat16 and tuple(out.shape) == (tokens, heads, width) and out.is_contiguous()
-              and out.device == dev):
-            raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({tokens}, {heads}, {width})")
-    if lse is not None:
-        if not (lse.dtype == torch.float32 and tuple(lse.shape) == (tokens, heads) and lse.is_contiguous()
-              and lse.device == dev):
-            raise ValueError(f"lse must be a contiguous float32 tensor of shape ({tokens}, {heads})")
+    if out is not None and not _is(out, _BFLOAT16, (tokens, heads, width), at):
+        raise ValueError(f"out must be a contiguous bfloat16 tensor of shape ({tokens}, {heads}, {width})")
+    if lse is not None and not _is(lse, _FLOAT32, (tokens, heads), at):
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape ({tokens}, {heads})")
 
 
 def _made(out, lse, tokens: int, heads: int, width: int, dev):
     if out is None:
-        out = torch.empty((tokens, heads, width), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((tokens, heads, width), dtype=_BFLOAT16, device=dev)
     if lse is None:
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
+        lse = torch.empty((tokens, heads), dtype=_FLOAT32, device=dev)
     return out, lse
 
 
@@ -183,18 +194,18 @@ def paged_append_plan(kv_lens, new_lens, page_table, free_pages, page_size: int,
     tokens are -1.  Returns AppendPlan; free_used above F says that pages ran
     out (their entries and slots are -1).
     """
-    dev = _gpu(kv_lens, "kv_lens")
+    dev, at = _gpu(kv_lens, "kv_lens")
     B = kv_lens.numel()
-    _int32("kv_lens", kv_lens, (B,), dev)
-    _int32("new_lens", new_lens, (B,), dev)
+    _int32("kv_lens", kv_lens, (B,), at)
+    _int32("new_lens", new_lens, (B,), at)
     if not (page_table.dim() == 2 and page_table.shape[0] == B):
         raise ValueError("page_table must be (requests, pages)")
-    _int32("page_table", page_table, tuple(page_table.shape), dev)
+    _int32("page_table", page_table, page_table.shape, at)
     if free_pages.dim() != 1:
         raise ValueError("free_pages must be 1-D")
-    _int32("free_pages", free_pages, tuple(free_pages.shape), dev)
+    _int32("free_pages", free_pages, free_pages.shape, at)
     if free_used is not None:
-        _int32("free_used", free_used, (1,), dev)
+        _int32("free_used", free_used, (1,), at)
     num_tokens = int(num_tokens)
     if num_tokens < 0:
         raise ValueError("num_tokens must be >= 0")
@@ -202,12 +213,12 @@ def paged_append_plan(kv_lens, new_lens, page_table, free_pages, page_size: int,
 
     def args(handle):
         # one allocation for all: these calls take microseconds
-        whole = torch.empty(2 * B + 2 + 2 * num_tokens, dtype=torch.int32, device=dev)
+        whole = torch.empty(2 * B + 2 + 2 * num_tokens, dtype=_INT32, device=dev)
         plan.append(AppendPlan(*whole.split_with_sizes((B, B + 1, num_tokens, num_tokens, 1))))
-        at = whole.data_ptr()
+        to = whole.data_ptr()
         return (kv_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), free_pages.data_ptr(),
-                free_used.data_ptr() if free_used is not None else None, int(page_size), at, at + 4 * B,
-                at + 4 * (2 * B + 1), at + 4 * (2 * B + 1 + num_tokens), at + 4 * (2 * B + 1 + 2 * num_tokens), handle,
+                free_used.data_ptr() if free_used is not None else None, int(page_size), to, to + 4 * B,
+                to + 4 * (2 * B + 1), to + 4 * (2 * B + 1 + num_tokens), to + 4 * (2 * B + 1 + 2 * num_tokens), handle,
                 B, page_table.shape[1], free_pages.shape[0], num_tokens)
 
     _call("paged_append_plan", dev, stream, args)
@@ -226,42 +237,40 @@ def latent_cache_store(kv, slot_map, latent, rope, scale=None, norm_weight=None,
     norm_weight (512,) bfloat16; positions (T,) int32; cos_sin (positions, 64)
     float32: cosines, then sines, of a position's 32 angles.
     """
-    dev = _gpu(kv, "kv")
-    if not (kv.dim() == 2 and kv.shape[1] == _QUERY and kv.dtype == torch.bfloat16 and kv.stride(1) == 1):
+    dev, at = _gpu(kv, "kv")
+    shape, strides = kv.shape, kv.stride()
+    if not (len(shape) == 2 and shape[1] == _QUERY and kv.dtype is _BFLOAT16 and strides[1] == 1):
         raise ValueError(f"kv must be a (tokens, {_QUERY}) bfloat16 tensor with contiguous rows")
-    T = kv.shape[0]
-    _int32("slot_map", slot_map, (T,), dev)
-    cache, slots = _cache(latent, rope, scale, dev)
+    T = shape[0]
+    _int32("slot_map", slot_map, (T,), at)
+    cache, slots = _cache(latent, rope, scale, at)
     if norm_weight is not None:
-        if not (norm_weight.dtype == torch.bfloat16 and tuple(norm_weight.shape) == (LATENT_DIM,)
-              and norm_weight.is_contiguous() and norm_weight.device == dev):
+        if not _is(norm_weight, _BFLOAT16, (LATENT_DIM,), at):
             raise ValueError(f"norm_weight must be a contiguous bfloat16 tensor of shape ({LATENT_DIM},)")
     if (positions is None) != (cos_sin is None):
         raise ValueError("positions and cos_sin go together")
     if cos_sin is not None:
-        _int32("positions", positions, (T,), dev)
-        if not (cos_sin.dim() == 2 and cos_sin.shape[1] == LATENT_ROPE_DIM and cos_sin.dtype == torch.float32
-              and cos_sin.is_contiguous() and cos_sin.device == dev):
+        _int32("positions", positions, (T,), at)
+        if not (cos_sin.dim() == 2 and _is(cos_sin, _FLOAT32, (cos_sin.shape[0], LATENT_ROPE_DIM), at)):
             raise ValueError(f"cos_sin must be a contiguous (positions, {LATENT_ROPE_DIM}) float32 tensor")
     rotate = cos_sin is not None
     _call("latent_cache_store", dev, stream, lambda handle: (
-        kv.data_ptr(), kv.stride(0) if T > 1 else _QUERY, norm_weight.data_ptr() if norm_weight is not None else None,
+        kv.data_ptr(), strides[0] if T > 1 else _QUERY, norm_weight.data_ptr() if norm_weight is not None else None,
         float(eps), positions.data_ptr() if rotate else None, cos_sin.data_ptr() if rotate else None,
         cos_sin.shape[0] if rotate else 0, int(bool(interleaved)), slot_map.data_ptr(), *cache, handle, T, slots))
 
 
-def _load_outputs(out_latent, out_rope, rows: int, dev):
+def _load_outputs(out_latent, out_rope, rows: int, at: int):
     for name, t, width in (("out_latent", out_latent, LATENT_DIM), ("out_rope", out_rope, LATENT_ROPE_DIM)):
-        if not (t is None or (t.dtype == torch.bfloat16 and tuple(t.shape) == (rows, width) and t.is_contiguous()
-                            and t.device == dev)):
+        if not (t is None or _is(t, _BFLOAT16, (rows, width), at)):
             raise ValueError(f"{name} must be a contiguous bfloat16 tensor of shape ({rows}, {width})")
 
 
 def _load_made(out_latent, out_rope, rows: int, dev):
     if out_latent is None:
-        out_latent = torch.empty((rows, LATENT_DIM), dtype=torch.bfloat16, device=dev)
+        out_latent = torch.empty((rows, LATENT_DIM), dtype=_BFLOAT16, device=dev)
     if out_rope is None:
-        out_rope = torch.empty((rows, LATENT_ROPE_DIM), dtype=torch.bfloat16, device=dev)
+        out_rope = torch.empty((rows, LATENT_ROPE_DIM), dtype=_BFLOAT16, device=dev)
     return out_latent, out_rope
 
 
@@ -269,13 +278,13 @@ def latent_cache_load(slots, latent, rope, scale=None, out_latent=None, out_rope
                       stream=None) -> Tuple[object, object]:
     """Rows of the cache by slot, as contiguous bfloat16: (rows, 512) and (rows,
     64).  slots (rows,) int32; a slot outside the cache gives zeros."""
-    dev = _gpu(slots, "slots")
+    dev, at = _gpu(slots, "slots")
     if slots.dim() != 1:
         raise ValueError("slots must be 1-D")
     rows = slots.shape[0]
-    _int32("slots", slots, (rows,), dev)
-    cache, n = _cache(latent, rope, scale, dev)
-    _load_outputs(out_latent, out_rope, rows, dev)
+    _int32("slots", slots, (rows,), at)
+    cache, n = _cache(latent, rope, scale, at)
+    _load_outputs(out_latent, out_rope, rows, at)
     got = []
 
     def args(handle):
@@ -292,17 +301,17 @@ def latent_cache_load_paged(page_table, kv_starts, page_size: int, num_rows: int
     [kv_starts[b], kv_starts[b + 1]) are positions 0, 1, ... of request b.
     page_table (B, P) int32, kv_starts (B + 1,) int32; num_rows is the length
     of the outputs, and rows past kv_starts[B] are left as they are."""
-    dev = _gpu(page_table, "page_table")
+    dev, at = _gpu(page_table, "page_table")
     if page_table.dim() != 2:
         raise ValueError("page_table must be (requests, pages)")
     B = page_table.shape[0]
-    _int32("page_table", page_table, tuple(page_table.shape), dev)
-    _int32("kv_starts", kv_starts, (B + 1,), dev)
+    _int32("page_table", page_table, page_table.shape, at)
+    _int32("kv_starts", kv_starts, (B + 1,), at)
     rows = int(num_rows)
     if rows < 0:
         raise ValueError("num_rows must be >= 0")
-    cache, n = _cache(latent, rope, scale, dev)
-    _load_outputs(out_latent, out_rope, rows, dev)
+    cache, n = _cache(latent, rope, scale, at)
+    _load_outputs(out_latent, out_rope, rows, at)
     got = []
 
     def args(handle):
@@ -324,14 +333,14 @@ def latent_attention(q, latent, rope, indices, softmax_scale: float, scale=None,
     (T, H) float32, the natural logarithm of the softmax's sum.  A token that
     selects nothing gets zeros and -inf.
     """
-    dev = _gpu(q, "q")
+    dev, at = _gpu(q, "q")
     T, H, qargs = _queries(q, _QUERY)
     if indices.dim() != 2:
         raise ValueError("indices must be (tokens, k)")
     k = indices.shape[1]
-    _int32("indices", indices, (T, k), dev)
-    cache, slots = _cache(latent, rope, scale, dev)
-    _outputs(out, lse, T, H, LATENT_DIM, dev)
+    _int32("indices", indices, (T, k), at)
+    cache, slots = _cache(latent, rope, scale, at)
+    _outputs(out, lse, T, H, LATENT_DIM, at)
     got = []
 
     def args(handle):
@@ -354,16 +363,16 @@ def latent_attention_paged(q, latent, rope, page_table, seq_lens, q_starts, page
     and their outputs are left as they are.  Other arguments and the return
     value as in latent_attention.
     """
-    dev = _gpu(q, "q")
+    dev, at = _gpu(q, "q")
     T, H, qargs = _queries(q, _QUERY)
     if page_table.dim() != 2:
         raise ValueError("page_table must be (requests, pages)")
     B, P = page_table.shape
-    _int32("page_table", page_table, (B, P), dev)
-    _int32("seq_lens", seq_lens, (B,), dev)
-    _int32("q_starts", q_starts, (B + 1,), dev)
-    cache, slots = _cache(latent, rope, scale, dev)
-    _outputs(out, lse, T, H, LATENT_DIM, dev)
+    _int32("page_table", page_table, (B, P), at)
+    _int32("seq_lens", seq_lens, (B,), at)
+    _int32("q_starts", q_starts, (B + 1,), at)
+    cache, slots = _cache(latent, rope, scale, at)
+    _outputs(out, lse, T, H, LATENT_DIM, at)
     got = []
 
     def args(handle):
@@ -387,7 +396,7 @@ def latent_attention_expanded(q, kv_up, rope, q_starts, kv_starts, softmax_scale
     out (Tq, H, 128) bfloat16 and lse (Tq, H) float32; a query with no key
     gets zeros and -inf, rows past q_starts[B] are left as they are.
     """
-    dev = _gpu(q, "q")
+    dev, at = _gpu(q, "q")
     T, H, qargs = _queries(q, LATENT_HEAD_DIM + LATENT_ROPE_DIM)
     if not (kv_up.dim() == 3 and tuple(kv_up.shape[1:]) == (H, 2 * LATENT_HEAD_DIM) and kv_up.dtype == torch.bfloat16
           and (kv_up.stride(2) == 1 or kv_up.numel() == 0) and kv_up.device == dev):
@@ -399,9 +408,9 @@ def latent_attention_expanded(q, kv_up, rope, q_starts, kv_starts, softmax_scale
     if not (q_starts.dim() == 1 and q_starts.shape[0] >= 1):
         raise ValueError("q_starts must be (requests + 1,)")
     B = q_starts.shape[0] - 1
-    _int32("q_starts", q_starts, (B + 1,), dev)
-    _int32("kv_starts", kv_starts, (B + 1,), dev)
-    _outputs(out, lse, T, H, LATENT_HEAD_DIM, dev)
+    _int32("q_starts", q_starts, (B + 1,), at)
+    _int32("kv_starts", kv_starts, (B + 1,), at)
+    _outputs(out, lse, T, H, LATENT_HEAD_DIM, at)
     got = []
 
     def args(handle):
