@@ -122,21 +122,33 @@ __device__ __forceinline__ int slot_of(const AttendArgs& a, const TokenKeys& tk,
 }
 
 // Tiles of [first, last) up to the last one that has a selected key; wave-uniform.
+constexpr int kScan = 256;             // entries looked at together
+struct ScanBlock {
+  int slot[kScan / 64];
+};
+__device__ __forceinline__ void load_scan(const TokenKeys& tk, int64_t begin, int64_t base, int lane, ScanBlock& s) {
+#pragma unroll
+  for (int i = 0; i < kScan / 64; ++i) {
+    const int64_t at = base - 1 - i * 64 - lane;
+    s.slot[i] = at >= begin ? tk.list[at] : -1;
+  }
+}
+__device__ __forceinline__ int64_t scan_begin(int64_t first) { return first * kTileKeys; }
+__device__ __forceinline__ int64_t scan_end(const TokenKeys& tk, int64_t last) {
+  return last * kTileKeys < tk.len ? last * kTileKeys : tk.len;
+}
+// s: the last block's entries.
 __device__ __forceinline__ int64_t selected_tiles(const AttendArgs& a, const TokenKeys& tk, int64_t first, int64_t last,
-                                                  int lane) {
-  const int64_t begin = first * kTileKeys, stop = last * kTileKeys < tk.len ? last * kTileKeys : tk.len;
-  // from the end, in blocks: most rows are full
-  for (int64_t base = stop; base > begin; base -= 256) {
-    uint64_t any[4];
+                                                  ScanBlock& s, int lane) {
+  const int64_t begin = scan_begin(first);
+  for (int64_t base = scan_end(tk, last); base > begin; base -= kScan) {
+    uint64_t any[kScan / 64];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = base - 1 - i * 64 - lane;
-      const int s = at >= begin ? tk.list[at] : -1;
-      any[i] = __ballot(s >= 0 && s < a.cache.num_slots);
-    }
+    for (int i = 0; i < kScan / 64; ++i) any[i] = __ballot(s.slot[i] >= 0 && s.slot[i] < a.cache.num_slots);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kScan / 64; ++i)
       if (any[i]) return (base - 1 - i * 64 - (int64_t)__builtin_ctzll(any[i])) / kTileKeys - first + 1;
+    load_scan(tk, begin, base - kScan, lane, s);
   }
   return 0;
 }
@@ -386,6 +398,35 @@ __device__ void plan_split(const AttendArgs& a, SplitPlan& plan, int tid) {
   lds_barrier();
 }
 
+// A wave's 16 rows of the output by way of LDS (`own`, the wave's), half a row
+// at a time: a lane holds 8-byte pieces of one row, and writes 16 bytes of
+// contiguous ones (16-byte chunks are flipped with their row, against bank conflicts).
+constexpr int kOutBytes = kHeads * kLatent;
+__device__ __forceinline__ void write_heads(const AttendArgs& a, int64_t token, int head0, const HeadState& st, float l,
+                                            char* own) {
+  const int lane = lane_here(), i = lane & 15, group = lane >> 4, chunk = lane & 31;
+  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const int64_t row = token * a.num_heads + head0;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int c = 0; c < kColBlocks / 2; ++c) {
+      bf16x4 v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = (__bf16)(st.o[half * (kColBlocks / 2) + c][r] * inv);
+      *reinterpret_cast<bf16x4*>(own + i * kLatent + (((2 * c + (group >> 1)) ^ i) << 4) + (group & 1) * 8) = v;
+    }
+#pragma unroll
+    for (int n = 0; n < kHeads / 2; ++n) {
+      const int r = 2 * n + (lane >> 5);
+      const uint4 v = *reinterpret_cast<const uint4*>(own + r * kLatent + ((chunk ^ r) << 4));
+      if (head0 + r < a.num_heads)
+        *reinterpret_cast<uint4*>(a.out + (row + r) * kLatent + half * (kLatent / 2) + chunk * 8) = v;
+    }
+  }
+  if (a.lse && group == 0 && head0 + i < a.num_heads) a.lse[row + i] = l > 0.f ? (st.m + __log2f(l)) * kLn2 : -INFINITY;
+}
+
 template <int NW, int RINGS, bool E4M3, bool PAGED>
 __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a) {
   using L = Lds<NW, RINGS, E4M3>;
@@ -461,23 +502,6 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
     const int64_t first = lo - start, last = hi - start < n ? hi - start : n;
     const bool whole = first == 0 && last == n;
 
-    HeadState st;
-    st.m = kNoMax;
-    st.l = 0.f;
-#pragma unroll
-    for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x4{};
-    {
-      // a negative scale goes into the signs of q: the largest product is then the largest score
-      const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-      const uint16_t* q = a.q + t * a.q_token_stride + (int64_t)head * a.q_head_stride + group * 8;
-#pragma unroll
-      for (int k = 0; k < kLatentSteps + kRopeSteps; ++k) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (head < a.num_heads) v = *reinterpret_cast<const uint4*>(q + k * 32);
-        st.q[k] = __builtin_bit_cast(bf16x8, make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign));
-      }
-    }
-
     // The ring: this wave's tiles are first + ring + RINGS i, tile i in stage i %
     // kStages; masks[d], the selected keys of the tile d after the one being
     // computed.  A tile's list entries are loaded one tile before its rows.
@@ -498,8 +522,26 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
     };
     lds_barrier();                        // the last part's reads are done
     if (tk.len > 0) load_entries(0);
+    ScanBlock scan;
+    if (!PAGED) load_scan(tk, scan_begin(first), scan_end(tk, last), lane, scan);
+
+    HeadState st;
+    st.m = kNoMax;
+    st.l = 0.f;
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x4{};
+    // the queries, on their way while the entries are waited for and the first rows queued
+    uint4 q[kLatentSteps + kRopeSteps];
+    {
+      const uint16_t* from = a.q + t * a.q_token_stride + (int64_t)head * a.q_head_stride + group * 8;
+#pragma unroll
+      for (int k = 0; k < kLatentSteps + kRopeSteps; ++k) {
+        q[k] = make_uint4(0, 0, 0, 0);
+        if (head < a.num_heads) q[k] = *reinterpret_cast<const uint4*>(from + k * 32);
+      }
+    }
     // Tiles past the part's last selected key hold nothing (a short row's tail).
-    const int64_t tiles = PAGED ? (tk.len > 0 ? last - first : 0) : selected_tiles(a, tk, first, last, lane);
+    const int64_t tiles = PAGED ? (tk.len > 0 ? last - first : 0) : selected_tiles(a, tk, first, last, scan, lane);
     const int mine = __builtin_amdgcn_readfirstlane((int)tiles) - ring;        // this ring's are the i with RINGS i < mine
     auto queue = [&](int i, uint32_t& mask) {
       if (L::kAhead > 1) entry = read_lds<int>(own_entries + (uint32_t)(i & 1) * 128 + (lane_here() & 31) * 4);
@@ -522,6 +564,11 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
         if (d + 1 < L::kAhead) wait_loads<L::kLoads>();        // the next entries
       }
     }
+    // a negative scale goes into the signs of q: the largest product is then the largest score
+    const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int k = 0; k < kLatentSteps + kRopeSteps; ++k)
+      st.q[k] = __builtin_bit_cast(bf16x8, make_uint4(q[k].x ^ sign, q[k].y ^ sign, q[k].z ^ sign, q[k].w ^ sign));
     int from = 0;                         // the stage of the tile being computed
     for (int i = 0; RINGS * i < mine + ring; ++i) {
       if (L::kAhead > 1 && RINGS * (i + 1) < mine)
@@ -568,19 +615,8 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
     // this lane's head: its sum is spread over four lanes
     const float l = sum_of_4(st.l);
     if (whole) {
-      if (writes && head < a.num_heads) {
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
-        const int64_t row = t * a.num_heads + head;
-        uint16_t* out = a.out + row * kLatent + 4 * group;
-#pragma unroll
-        for (int cb = 0; cb < kColBlocks; ++cb) {
-          bf16x4 v;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = (__bf16)(st.o[cb][r] * inv);
-          *reinterpret_cast<bf16x4*>(out + cb * 16) = v;
-        }
-        if (a.lse && group == 0) a.lse[row] = l > 0.f ? (st.m + __log2f(l)) * kLn2 : -INFINITY;
-      }
+      if (RINGS == 1) lds_barrier();      // nobody reads the stages any more
+      if (writes && live_wave) write_heads(a, t, (block * NW + wave) * kHeads, st, l, lds + wave * (RINGS > 1 ? kHeads * kLatent * 4 : kOutBytes));
       if (split && tid == 0 && block == 0) {
         a.part_rec[2 * t] = 0;
         a.part_rec[2 * t + 1] = 1;
