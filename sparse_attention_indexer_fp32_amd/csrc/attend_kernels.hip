@@ -160,25 +160,34 @@ __device__ __forceinline__ int code_swizzle(int row) {
   return (row & 3) | ((row ^ (row >> 2)) & 4) | (row & 8);
 }
 
-// A slot's row; zeros for a slot below 0.  (Selected, not branched on: a tile
-// takes 32 of them.)
+// A slot's row; zeros for a slot below 0.  (Selected, not branched on: a tile takes 32 of them.)
 __device__ __forceinline__ const char* row_at(const char* base, int64_t stride, int slot) {
   return (slot < 0 ? kZeroRow : base) + (int64_t)(slot < 0 ? 0 : slot) * stride;
 }
 
+// Lane `from`'s address, in every lane.
+__device__ __forceinline__ const char* row_of(const char* rows, int from) {
+  const uint64_t v = (uint64_t)(uintptr_t)rows;
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, from), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), from);
+  return reinterpret_cast<const char*>((uintptr_t)((uint64_t)hi << 32 | lo));
+}
+
 // Queues the loads of a tile's rows into the stage at LDS address `lds`;
-// `slots`: lane i (mod 32) holds key i's.
+// `slots`: lane i (mod 32) holds key i's.  Every lane forms the address of its own
+// key's row, and a load takes it from there by two lane reads: formed one row
+// after the other, the addresses took as long to queue as the tile to compute
+// where one wave loads all rows.
 template <int NW, bool E4M3>
 __device__ __forceinline__ void load_tile(const Cache& c, int slots, uint32_t lds, int wave) {
   const int lane = lane_here();
+  const char* rows = row_at(c.latent, c.latent_stride, slots);
   if (E4M3) {
     constexpr int kEach = kTileKeys / 2 / NW;   // two rows an instruction
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int pair = wave * kEach + i;
-      const int s0 = __builtin_amdgcn_readlane(slots, 2 * pair), s1 = __builtin_amdgcn_readlane(slots, 2 * pair + 1);
-      const char* r0 = row_at(c.latent, c.latent_stride, s0);
-      const char* r1 = row_at(c.latent, c.latent_stride, s1);
+      const char* r0 = row_of(rows, 2 * pair);
+      const char* r1 = row_of(rows, 2 * pair + 1);
       const int sw = lane < 32 ? code_swizzle(2 * pair) : code_swizzle(2 * pair + 1);
       queue_to_lds((lane < 32 ? r0 : r1) + ((lane & 31) ^ sw) * 16, lds + pair * 2 * kLatent);
     }
@@ -187,9 +196,7 @@ __device__ __forceinline__ void load_tile(const Cache& c, int slots, uint32_t ld
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int key = wave * kEach + i;
-      const int s = __builtin_amdgcn_readlane(slots, key);
-      const char* row = row_at(c.latent, c.latent_stride, s);
-      queue_to_lds(row, (uint32_t)(lane ^ swizzle(key)) * 16, lds + key * kRowBytes);
+      queue_to_lds(row_of(rows, key) + (lane ^ swizzle(key)) * 16, lds + key * kRowBytes);
     }
   }
   lds += E4M3 ? kTileCodes : kTileLatent;

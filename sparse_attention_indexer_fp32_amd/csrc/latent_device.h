@@ -106,10 +106,6 @@ __device__ __forceinline__ void load_to_lds(const char* src, char* dst) {
 // load into the same array, and a ring of stages in one array is such.  The
 // caller waits (wait_loads) and passes a barrier before it reads the bytes.
 // lds: byte address in LDS.
-__device__ __forceinline__ void queue_to_lds(const char* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(offset), "s"(base), "s"(lds) : "m0", "memory");
-}
 __device__ __forceinline__ void queue_to_lds(const char* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :: "v"(src), "s"(lds) : "m0", "memory");
