@@ -73,7 +73,7 @@ struct Lds {
   static constexpr int kStages = kAhead + 1;
   static constexpr int kScales = kStages * kStageBytes;                       // a wave's own: 32 a stage
   static constexpr int kEntries = kScales + (E4M3 ? NW * kStages * 128 : 0);  // a wave's own: two tiles
-  static constexpr int kRingBytes = (kEntries + (kAhead > 1 ? NW * 2 * 128 : 0) + 255) / 256 * 256;
+  static constexpr int kRingBytes = (kEntries + NW * 2 * 128 + 255) / 256 * 256;
   // joining: the second ring's waves' accumulators, then their maxima and sums
   static constexpr int kJoinBytes = RINGS > 1 ? NW * (kHeads * kLatent * 4 + 512) : 0;
   static constexpr int kBytes = RINGS * kRingBytes > kJoinBytes ? RINGS * kRingBytes : kJoinBytes;
@@ -90,11 +90,24 @@ struct HeadState {
   float l;      // this lane's part of the sum
 };
 
-// Of a split launch's workgroups, those that take part.
-__device__ __forceinline__ int shares_of(const AttendArgs& a, int64_t tiles) {
-  const int64_t most = tiles / kShareTiles;
-  return most < 1 ? 1 : most < a.wgs ? (int)most : a.wgs;
-}
+// A split launch's tiles, dealt evenly: the first `more` shares hold each + 1,
+// the others `each`, in order.  (32-bit divisions: a 64-bit one is hundreds of
+// instructions, which a launch of a few tiles waits for to be fetched.)
+struct Shares {
+  uint32_t count, each, more;
+  __device__ __forceinline__ explicit Shares(const AttendArgs& a, uint32_t tiles) {
+    const uint32_t most = tiles / kShareTiles;
+    count = most < 1 ? 1 : most < (uint32_t)a.wgs ? most : (uint32_t)a.wgs;
+    each = tiles / count;
+    more = tiles - each * count;
+  }
+  __device__ __forceinline__ int begin(uint32_t share) const { return (int)(share * each + (share < more ? share : more)); }
+  // the share that holds a tile
+  __device__ __forceinline__ int owner(uint32_t tile) const {
+    const uint32_t longer = more * (each + 1);
+    return (int)(tile < longer ? tile / (each + 1) : more + (tile - longer) / each);
+  }
+};
 
 // Where the keys of a token come from.
 struct TokenKeys {
@@ -444,26 +457,31 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
   // Workgroups are dealt to the 8 XCDs in turn.  The head blocks of the same keys
   // follow each other on one XCD, so that all but the first find the rows in its L2.
   const int blocks = (a.num_heads + kHeads * NW - 1) / (kHeads * NW);
-  const int xcd = blockIdx.x & 7, nth = (int)(blockIdx.x >> 3) / blocks, block = (int)(blockIdx.x >> 3) % blocks;
-  const int head = (block * NW + wave) * kHeads + (lane & 15), group = lane >> 4;
+  const int xcd = blockIdx.x & 7, nth = (int)((blockIdx.x >> 3) / (unsigned)blocks);
+  const int block = (int)(blockIdx.x >> 3) - nth * blocks;
   const bool live_wave = (block * NW + wave) * kHeads < a.num_heads;
   constexpr bool split = RINGS > 1;
   const int share = nth * 8 + xcd;      // split: this workgroup's number among those of its head block
 
   // this workgroup's tiles [lo, hi) of all tokens' tiles, beginning in token
   // t, whose first tile is number `start` and whose request is b
-  int64_t lo = 0, hi = INT64_MAX, t, start = 0, total = 0, b = 0;
-  int wgs = 1;
-  const int64_t k_tiles = token_tiles(a.k);
+  int lo = 0, hi = INT32_MAX, start = 0;
+  int64_t t, b = 0;
+  uint32_t total = 0;
   if (split) {
+    const uint32_t k_tiles = (uint32_t)token_tiles(a.k);
     if (PAGED) {
-      SplitPlan& plan = *reinterpret_cast<SplitPlan*>(lds);
-      plan_split<NW * RINGS>(a, plan, tid);
-      total = __builtin_amdgcn_readfirstlane(plan.start[a.num_tokens]);
-      wgs = shares_of(a, total);
-      if (share >= wgs) return;
-      lo = total * share / wgs;
-      hi = total * (share + 1) / wgs;
+      plan_split<NW * RINGS>(a, *reinterpret_cast<SplitPlan*>(lds), tid);
+      total = (uint32_t)__builtin_amdgcn_readfirstlane(reinterpret_cast<SplitPlan*>(lds)->start[a.num_tokens]);
+    } else {
+      total = (uint32_t)a.num_tokens * k_tiles;
+    }
+    const Shares shares(a, total);
+    if ((uint32_t)share >= shares.count) return;
+    lo = __builtin_amdgcn_readfirstlane(shares.begin(share));
+    hi = __builtin_amdgcn_readfirstlane(shares.begin(share + 1));
+    if (PAGED) {
+      const SplitPlan& plan = *reinterpret_cast<SplitPlan*>(lds);
       int l = 0, h = a.num_tokens;
       while (h - l > 1) {
         const int mid = (l + h) >> 1;
@@ -473,13 +491,8 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
       start = __builtin_amdgcn_readfirstlane(plan.start[t]);
       b = __builtin_amdgcn_readfirstlane((int)plan.request[t]);
     } else {
-      total = a.num_tokens * k_tiles;
-      wgs = shares_of(a, total);
-      if (share >= wgs) return;
-      lo = total * share / wgs;
-      hi = total * (share + 1) / wgs;
-      t = lo / k_tiles;
-      start = t * k_tiles;
+      t = __builtin_amdgcn_readfirstlane((uint32_t)lo / k_tiles);
+      start = (int)t * (int)k_tiles;
     }
   } else {
     // neighbouring tokens select neighbouring rows: each XCD takes a contiguous
@@ -505,53 +518,44 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
       tk.len = a.k;
       tk.list = a.indices + t * a.k;
     }
-    const int64_t n = token_tiles(tk.len);
-    const int64_t first = lo - start, last = hi - start < n ? hi - start : n;
+    const int n = (int)token_tiles(tk.len);
+    const int first = lo - start, last = hi - start < n ? hi - start : n;
     const bool whole = first == 0 && last == n;
 
     // The ring: this wave's tiles are first + ring + RINGS i, tile i in stage i %
     // kStages; masks[d], the selected keys of the tile d after the one being
     // computed.  A tile's list entries are loaded one tile before its rows.
-    // With two tiles on their way, entries and scales too are loaded into LDS,
-    // so that no load in the loop is the compiler's to wait for.
+    // Entries (and scales) too are loaded into LDS, so that no load in the loop is
+    // the compiler's to wait for: it would wait for the rows queued behind it.
     uint32_t masks[L::kAhead + 1];
-    int entry = 0;                        // kAhead == 1: of the tile to be queued next
     int into = 0;                         // the stage of the tile to be queued next
     const uint32_t own_entries = lds_base + L::kEntries + wave * 256;
     const uint32_t scales = lds_base + L::kScales + wave * L::kStages * 128;
-    auto tile_of = [&](int i) { return first + ring + RINGS * i; };
+    auto tile_of = [&](int i) { return (int64_t)(first + ring + RINGS * i); };
     auto load_entries = [&](int i) {
-      const int32_t* at = entry_of<PAGED>(a, tk, tile_of(i));
-      if (L::kAhead > 1)
-        queue_words_to_lds(at, own_entries + (uint32_t)(i & 1) * 128);
-      else
-        entry = *at;
+      queue_words_to_lds(entry_of<PAGED>(a, tk, tile_of(i)), own_entries + (uint32_t)(i & 1) * 128);
     };
     lds_barrier();                        // the last part's reads are done
     if (tk.len > 0) load_entries(0);
     ScanBlock scan;
-    if (!PAGED) load_scan(tk, scan_begin(first), scan_end(tk, last), lane, scan);
+    if (!PAGED) load_scan(tk, scan_begin(first), scan_end(tk, last), lane_here(), scan);
 
-    HeadState st;
-    st.m = kNoMax;
-    st.l = 0.f;
-#pragma unroll
-    for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x4{};
-    // the queries, on their way while the entries are waited for and the first rows queued
+    // the queries (of a head past the last, the last's), on their way while the entries are waited for and the first rows queued
     uint4 q[kLatentSteps + kRopeSteps];
     {
-      const uint16_t* from = a.q + t * a.q_token_stride + (int64_t)head * a.q_head_stride + group * 8;
+      const int l = lane_here(), h = (block * NW + wave) * kHeads + (l & 15);
+      const uint16_t* from = a.q + t * a.q_token_stride + (int64_t)(h < a.num_heads ? h : a.num_heads - 1) * a.q_head_stride +
+                             (l >> 4) * 8;
 #pragma unroll
       for (int k = 0; k < kLatentSteps + kRopeSteps; ++k) {
-        q[k] = make_uint4(0, 0, 0, 0);
-        if (head < a.num_heads) q[k] = *reinterpret_cast<const uint4*>(from + k * 32);
+        q[k] = *reinterpret_cast<const uint4*>(from + k * 32);
       }
     }
     // Tiles past the part's last selected key hold nothing (a short row's tail).
-    const int64_t tiles = PAGED ? (tk.len > 0 ? last - first : 0) : selected_tiles(a, tk, first, last, scan, lane);
+    const int64_t tiles = PAGED ? (tk.len > 0 ? last - first : 0) : selected_tiles(a, tk, first, last, scan, lane_here());
     const int mine = __builtin_amdgcn_readfirstlane((int)tiles) - ring;        // this ring's are the i with RINGS i < mine
     auto queue = [&](int i, uint32_t& mask) {
-      if (L::kAhead > 1) entry = read_lds<int>(own_entries + (uint32_t)(i & 1) * 128 + (lane_here() & 31) * 4);
+      const int entry = read_lds<int>(own_entries + (uint32_t)(i & 1) * 128 + (lane_here() & 31) * 4);
       const int slot = slot_of<PAGED>(a, tk, entry, tile_of(i));
       mask = (uint32_t)__ballot(slot >= 0);
       if (RINGS * (i + 1) < mine) load_entries(i + 1);
@@ -562,7 +566,8 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
       load_tile<NW, E4M3>(a.cache, slot, lds_base + into * L::kStageBytes, wave);
       into = into + 1 < L::kStages ? into + 1 : 0;
     };
-    wait_loads<0>();                      // the entries
+    // The entries: with selected slots, whose scan was loaded after them, they are there.
+    if (PAGED) wait_loads<kLatentSteps + kRopeSteps>();
 #pragma unroll
     for (int d = 0; d < L::kAhead; ++d) {
       masks[d] = 0;
@@ -571,6 +576,11 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
         if (d + 1 < L::kAhead) wait_loads<L::kLoads>();        // the next entries
       }
     }
+    HeadState st;
+    st.m = kNoMax;
+    st.l = 0.f;
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] = f32x4{};
     // a negative scale goes into the signs of q: the largest product is then the largest score
     const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll
@@ -636,13 +646,14 @@ __global__ __launch_bounds__(64 * NW * RINGS, 2) void attend_kernel(AttendArgs a
         float* o = a.part_out + at * (kHeads * kLatent) + lane * 4;
 #pragma unroll
         for (int cb = 0; cb < kColBlocks; ++cb) *reinterpret_cast<f32x4*>(o + cb * 256) = st.o[cb];
-        if (group == 0) a.part_ml[at * kHeads + lane] = make_float2(st.m, l);
+        if (lane < kHeads) a.part_ml[at * kHeads + lane] = make_float2(st.m, l);
       }
       if (first == 0 && tid == 0 && block == 0) {
-        // the last of its tiles is held by the last workgroup g with total g / wgs <= that tile
-        const int64_t g1 = ((start + n) * wgs - 1) / total;
+        uint32_t again = total;           // (worked out here, not kept through the part)
+        asm volatile("" : "+s"(again));
+        const int g1 = Shares(a, again).owner((uint32_t)(start + n - 1));
         a.part_rec[2 * t] = share;
-        a.part_rec[2 * t + 1] = (int32_t)(g1 - share + 1);
+        a.part_rec[2 * t + 1] = g1 - share + 1;
       }
     }
     if (!split) return;
