@@ -27,7 +27,8 @@
  * `stream`, allocate nothing, keep no state between calls (a workspace is the
  * caller's, so calls on different streams, devices or captured graphs share
  * nothing unless the caller shares it) and may be captured.  bf16 arguments
- * are passed as uint16_t pointers.  Status codes and topk_last_error() are
+ * are passed as uint16_t pointers.  What a call writes must not overlap what it
+ * reads, but for the page table that is updated in place.  Status codes and topk_last_error() are
  * topk_transform.h's.  Errors of every call: TOPK_ERROR_INVALID_VALUE for a
  * negative size, a required pointer that is NULL, a page size that is not a
  * power of two, a misaligned pointer or stride; TOPK_ERROR_UNSUPPORTED on a
@@ -108,7 +109,7 @@ topk_status_t paged_append_plan(const int32_t* kv_lens, const int32_t* new_lens,
  *   positions   (num_tokens,) int32; read only with cos_sin.
  *   slot_map    (num_tokens,) int32.  Tokens with a slot outside [0, num_slots), or
  *               (with cos_sin) a position outside [0, max_positions), are not
- *               stored.  Of two tokens with one slot, either is stored.
+ *               stored.  No two tokens may name one slot (parts of either would be stored).
  * E4M3 caches: scale[slot] = max|y| / 448 (1 where y is all zero), codes =
  * y / scale rounded to nearest even.  A row whose y has a NaN or an infinity
  * reads back as NaN throughout (its scale is NaN).  All arithmetic

@@ -186,6 +186,8 @@ topk_status_t paged_append_plan(const int32_t* kv_lens, const int32_t* new_lens,
   if (!q_starts || !free_used_out) return invalid("q_starts and free_used_out must be non-null");
   if (free_used == free_used_out) return invalid("free_used_out must not be free_used");
   if (num_requests > 0 && (!kv_lens || !new_lens || !seq_lens)) return invalid("kv_lens, new_lens and seq_lens must be non-null");
+  if (num_requests > 0 && (seq_lens == kv_lens || seq_lens == new_lens))
+    return invalid("seq_lens must not be kv_lens or new_lens: other workgroups still read those");
   if (num_requests > 0 && pages_per_row > 0 && !page_table) return invalid("page_table must be non-null");
   if (num_free > 0 && !free_pages) return invalid("free_pages must be non-null");
   if (num_tokens > 0 && (!slot_map || !positions)) return invalid("slot_map and positions must be non-null");

@@ -231,11 +231,12 @@ def latent_cache_store(kv, slot_map, latent, rope, scale=None, norm_weight=None,
     rotation of the rotary key (with positions and cos_sin), 8-bit codes and a
     scale per token (with scale), in one pass.
 
-    kv (T, 512 + 64) bfloat16 with any row stride; slot_map (T,) int32, tokens
-    with a slot outside the cache are skipped; latent (slots, 512) bfloat16,
-    or uint8 codes with scale (slots,) float32; rope (slots, 64) bfloat16;
-    norm_weight (512,) bfloat16; positions (T,) int32; cos_sin (positions, 64)
-    float32: cosines, then sines, of a position's 32 angles.
+    kv (T, 512 + 64) bfloat16 with any row stride; slot_map (T,) int32: tokens
+    with a slot outside the cache are skipped, and no two may name one slot;
+    latent (slots, 512) bfloat16, or uint8 codes with scale (slots,) float32;
+    rope (slots, 64) bfloat16; norm_weight (512,) bfloat16; positions (T,)
+    int32; cos_sin (positions, 64) float32: cosines, then sines, of a
+    position's 32 angles.
     """
     dev, at = _gpu(kv, "kv")
     shape, strides = kv.shape, kv.stride()

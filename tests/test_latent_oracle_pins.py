@@ -102,7 +102,7 @@ A = 4096   # a pointer that is never followed: the calls below fail their checks
 
 
 def _plan(lib, **kw):
-    a = dict(kv=A, new=A, table=A, free=A, used=None, ps=16, seq=A, qs=A, slots=A, pos=A, out=A, B=2, P=2, F=2, T=4)
+    a = dict(kv=A, new=A, table=A, free=A, used=None, ps=16, seq=A + 256, qs=A, slots=A, pos=A, out=A, B=2, P=2, F=2, T=4)
     a.update(kw)
     return lib.paged_append_plan(a["kv"], a["new"], a["table"], a["free"], a["used"], a["ps"], a["seq"], a["qs"],
                                  a["slots"], a["pos"], a["out"], None, a["B"], a["P"], a["F"], a["T"])
@@ -111,7 +111,8 @@ def _plan(lib, **kw):
 @pytest.mark.parametrize("kw", [dict(ps=0), dict(ps=-4), dict(ps=24), dict(B=-1), dict(P=-1), dict(F=-1), dict(T=-1),
                                 dict(T=2 ** 31), dict(kv=None), dict(new=None), dict(table=None), dict(free=None),
                                 dict(seq=None), dict(qs=None), dict(slots=None), dict(pos=None), dict(out=None),
-                                dict(used=A)])   # free_used_out aliases free_used
+                                dict(used=A),                   # free_used_out aliases free_used
+                                dict(seq=A), dict(new=A + 256)])   # seq_lens aliases kv_lens, new_lens
 def test_plan_refusals(lib, kw):
     assert _plan(lib, **kw) == 1 and topk.topk_last_error()
 
