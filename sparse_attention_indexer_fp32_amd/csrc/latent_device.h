@@ -190,7 +190,6 @@ __device__ __forceinline__ float sum_of_4(float v) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 // Initial reference maximum of a running softmax: finite, so that masked
 // scores (-inf) give weights of exactly 0 and never inf - inf.
