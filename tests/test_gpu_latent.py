@@ -314,6 +314,23 @@ def test_selected_large_scores(lib, dev):
             _check_token(f"scale {scale} token {t}", cache, qh[t], idx[t], scale, _host(out)[t], _host(lse)[t])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_selected_long_list_of_few_slots(lib, dev, e4m3):
+    """A list far longer than the cache, one slot many times: every naming counts,
+    shared by as many workgroups as there are.  Also at scale 0, where all count alike."""
+    rng = np.random.default_rng(10)
+    cache = Cache(rng, 300, e4m3, dev)
+    q, qh = _bf(rng, (3, 20, 576), dev)
+    idx = rng.integers(0, 300, (3, 40000))
+    idx[1, 100:] = 7
+    idx[2, :39999] = -1                          # only the last entry
+    for scale in (0.1, 0.0):
+        out, lse = lib.latent_attention(q, cache.latent, cache.rope, _i32(idx, dev), scale, scale=cache.scale)
+        for t in range(3):
+            _check_token(f"scale {scale} token {t}", cache, qh[t], idx[t][idx[t] >= 0], scale, _host(out)[t], _host(lse)[t],
+                         heads=(0, 19))
+
+
 def test_selected_far_slots(lib, dev):
     """Slots whose byte offsets pass 2^32 (a cache of 9 GB)."""
     import torch
@@ -439,6 +456,27 @@ def test_expanded(lib, dev, name):
                 for err in (lo.check(f"{b} {i} {h} out", out[qs[b] + i, h], a.out, a.out_bound),
                             lo.check(f"{b} {i} {h} lse", lse[qs[b] + i, h], a.lse, a.lse_bound)):
                     assert err is None, err
+
+
+@pytest.mark.parametrize("nq,nk", [(70, 333), (40, 4500)])      # one workgroup to a block, and several
+@pytest.mark.parametrize("scale", [4.0, -1.0, 0.0])
+def test_expanded_scales(lib, dev, nq, nk, scale):
+    """Scores of hundreds, the largest products last, of both signs, and none."""
+    rng = np.random.default_rng(62)
+    q, qh = _bf(rng, (nq, 2, 192), dev)
+    kv, kvh = _bf(rng, (nk, 2, 256), dev)
+    rope, rh = _bf(rng, (nk, 64), dev)
+    order = np.argsort(np.concatenate([kvh[:, 0, :128], rh], 1) @ qh[nq - 1, 0])
+    at = _i32(order, dev).long()
+    kv, rope, kvh, rh = kv[at].contiguous(), rope[at].contiguous(), kvh[order], rh[order]
+    out, lse = lib.latent_attention_expanded(q, kv, rope, _i32([0, nq], dev), _i32([0, nk], dev), scale)
+    out, lse = _host(out), _host(lse)
+    for i in (0, 31, nq - 1):
+        n = lo.causal_keys(i, nq, nk, True)
+        for h in range(2):
+            a = lo.attend(qh[i, h], np.concatenate([kvh[:n, h, :128], rh[:n]], 1), kvh[:n, h, 128:], scale)
+            for err in (lo.check(f"{i} {h} out", out[i, h], a.out, a.out_bound), lo.check(f"{i} {h} lse", lse[i, h], a.lse, a.lse_bound)):
+                assert err is None, err
 
 
 def test_expanded_split_over_many_requests(lib, dev):
