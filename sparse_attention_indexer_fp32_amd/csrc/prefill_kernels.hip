@@ -27,8 +27,8 @@
 // the matrix cores are busy 50 % of the time, and the softmax's vector
 // instructions (157 to 40 matrix ones a tile, 32 of them exponentials) take the
 // other half; LDS 27 %.  Six chunks of 1 to 1500 tokens behind 0 to 5000 cached
-// ones x 20 heads 223 us, 745 TFLOP/s: bound by the longest units, 6500 keys at
-// 2.4 us a tile with two workgroups on a CU.  (The output written from the
+// ones x 20 heads 223-245 us, up to 745 TFLOP/s: bound by the longest units, 6500
+// keys at 2.4 us a tile with two workgroups on a CU.  (The output written from the
 // accumulators, 8 bytes a lane, and lane offsets that did not fit the registers
 // cost 743 us instead of 716; head after head instead of block after block 738
 // instead of 691.)
