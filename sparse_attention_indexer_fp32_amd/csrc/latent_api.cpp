@@ -97,10 +97,12 @@ float scale_log2(float softmax_scale) {
 // workgroup per token.  Not split, two workgroups run on a CU at a time, and the
 // last round of them may leave most CUs idle: split is what leaves more than a
 // third idle (64 heads, 2048 selected bf16 slots, us split and not: 300 tokens
-// 153 and 160, 512 tokens 217 and 203; 700 tokens of 8-bit slots 362 and 339).
-// With 32 heads, split launches are the faster ones throughout (512 tokens 185
-// and 206, 2048 tokens 700 and 728, 8-bit 687 and 789); with 16 they are not
-// (1024 tokens 449 and 427).
+// 143 and 150, 400 tokens 195 and 158, 512 tokens 196 and 178; 700 tokens of 8-bit
+// slots 366 and 333).  With 32 heads split launches are the faster ones where rounds
+// are not full (700 tokens 237 and 286) and with 8-bit slots (512 tokens 184 and
+// 222, 2048 tokens 689 and 817), and as fast otherwise (512 tokens 173 and 172,
+// 2048 tokens 669 and 656), so all of them are; with 16 heads they are not
+// (1024 tokens 336 and 331, 8-bit 361 and 330).
 // A workgroup takes kShareTiles tiles or more: one token of 64 tiles x 128 heads
 // took 27.8 us at one tile to a workgroup, 22.3 at two and 21.9 at four; 4 tokens
 // x 64 heads 31.6, 26.6 and 25.3.
