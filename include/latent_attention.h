@@ -161,7 +161,10 @@ topk_status_t latent_cache_load_paged(const int32_t* page_table, const int32_t* 
  *   lse      (num_tokens, num_heads) fp32 or NULL, written: the natural
  *            logarithm of the sum of exponentials.
  * A token that selects nothing gets zeros in out and -inf in lse.  What the
- * cache holds in slots that are not selected is never used, NaN included.
+ * cache holds in slots that are not selected is never used, NaN included.  A
+ * selected row that makes a head's score NaN (the NaN scale of an E4M3 row
+ * among others) or +inf makes that head's out and lse NaN; a score of -inf
+ * weighs nothing.
  * Scores, statistics and sums are fp32; the weights are rounded to bf16 for
  * the matrix cores, and the result once at the end.
  *
@@ -218,7 +221,8 @@ topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, 
  *            its request's nk; 0: all of them.
  *   out      (num_tokens, num_heads, LATENT_HEAD_DIM) bf16; lse (num_tokens,
  *            num_heads) fp32 or NULL: as latent_attention.
- * A query with no key gets zeros and -inf.  Rows of q from
+ * A query with no key gets zeros and -inf, one with a score that is NaN or
+ * +inf gets NaN in both.  Rows of q from
  * q_starts[num_requests] on are left as they are in out and lse; key rows from
  * kv_starts[num_requests] on are not read.  The workspace is
  * latent_attention_expanded_workspace's, otherwise as latent_attention's.

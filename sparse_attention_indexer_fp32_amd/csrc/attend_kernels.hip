@@ -438,7 +438,7 @@ constexpr int kOutBytes = kHeads * kLatent;
 __device__ __forceinline__ void write_heads(const AttendArgs& a, int64_t token, int head0, const HeadState& st, float l,
                                             char* own) {
   const int lane = lane_here(), i = lane & 15, group = lane >> 4, chunk = lane & 31;
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = inverse_sum(l);
   const int64_t row = token * a.num_heads + head0;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -457,7 +457,7 @@ __device__ __forceinline__ void write_heads(const AttendArgs& a, int64_t token, 
         *reinterpret_cast<uint4*>(a.out + (row + r) * kLatent + half * (kLatent / 2) + chunk * 8) = v;
     }
   }
-  if (a.lse && group == 0 && head0 + i < a.num_heads) a.lse[row + i] = l > 0.f ? (st.m + __log2f(l)) * kLn2 : -INFINITY;
+  if (a.lse && group == 0 && head0 + i < a.num_heads) a.lse[row + i] = log_sum(st.m, l);
 }
 
 template <int NW, int RINGS, bool E4M3, bool PAGED>
@@ -750,7 +750,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttendArgs a) {
   }
   const int head = heads * kHeads + i;
   if (head >= a.num_heads) return;
-  const float inv = st.l > 0.f ? 1.0f / st.l : 0.f;
+  const float inv = inverse_sum(st.l);
   const int64_t row = t * a.num_heads + head;
 #pragma unroll
   for (int c = 0; c < kJoinBlocks; ++c) {
@@ -759,7 +759,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(AttendArgs a) {
     for (int r = 0; r < 4; ++r) v[r] = (__bf16)(st.o[c][r] * inv);
     *reinterpret_cast<bf16x4*>(a.out + row * kLatent + (cb0 + c) * 16 + 4 * group) = v;
   }
-  if (a.lse && cb0 == 0 && group == 0) a.lse[row] = st.l > 0.f ? (st.m + __log2f(st.l)) * kLn2 : -INFINITY;
+  if (a.lse && cb0 == 0 && group == 0) a.lse[row] = log_sum(st.m, st.l);
 }
 
 int ceil_div(int a, int b) { return (int)(((int64_t)a + b - 1) / b); }

@@ -191,6 +191,13 @@ __device__ __forceinline__ float sum_of_4(float v) {
 }
 
 constexpr float kLn2 = 0.69314718055994530942f;
+// A row's results from its reference m (log2 units) and its sum l: what its
+// accumulators are multiplied by, and the logarithm of the sum of exponentials.
+// The sum is 0 only where nothing weighs anything: 0 and -inf.  It is NaN where a
+// score is NaN or +inf, and so are both results.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
+
 // Initial reference maximum of a running softmax: finite, so that masked
 // scores (-inf) give weights of exactly 0 and never inf - inf.
 constexpr float kNoMax = -1e30f;

@@ -423,15 +423,13 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
       [&](int n, bf16x8 cols) { st.o[n % kColBlocks] = mfma(cols, p[n / kColBlocks], st.o[n % kColBlocks]); });
 }
 
-__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY; }
-
 // A wave's 32 rows of the output, out_i = o_i / l, by way of LDS (`own`: 8 KB
 // of the wave's): a lane holds 8-byte pieces of one row, and writes 16 bytes of
 // whole rows (each 16-byte chunk is flipped with its row, against bank conflicts).
 __device__ __forceinline__ void write_rows(const PrefillArgs& a, const Block& blk, int64_t wave_row, int64_t head,
                                            const f32x16 (&o)[kColBlocks], float m, float l, char* own, int lane) {
   const int i = lane & 31, hb = lane >> 5;
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = inverse_sum(l);
 #pragma unroll
   for (int cb = 0; cb < kColBlocks; ++cb)
 #pragma unroll
@@ -656,7 +654,7 @@ __global__ __launch_bounds__(64 * kColBlocks) void prefill_join_kernel(PrefillAr
     }
   }
   if (row >= blk.nq) return;
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = inverse_sum(l);
   const int64_t at = (blk.q0 + row) * a.num_heads + head;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {

@@ -741,3 +741,71 @@ def test_small_workspace_is_refused(lib, dev):
     assert call(ws.data_ptr(), n.value) == 0
     torch.cuda.synchronize()
     assert torch.equal(out, lib.latent_attention(x["q"], x["cache"].latent, x["cache"].rope, x["idx"], 0.1)[0])
+
+
+# ---- attended keys that are not finite ----------------------------------------------------------------------
+
+# tokens, heads, keys: one workgroup a token; whole tokens shared among workgroups; parts joined by the second launch
+SHAPES = {"own": (350, 8, 70), "shared": (5, 24, 90), "joined": (5, 40, 2000)}
+
+
+def _both_absorbed(lib, dev, cache, q, idx, scale):
+    """The absorbed form over the slots of idx, by list and as pages of one slot."""
+    T, k = idx.shape
+    yield "selected", *lib.latent_attention(q, cache.latent, cache.rope, _i32(idx, dev), scale, scale=cache.scale)
+    yield "paged", *lib.latent_attention_paged(q, cache.latent, cache.rope, _i32(idx, dev), _i32([k] * T, dev),
+                                               _i32(range(T + 1), dev), 1, scale, scale=cache.scale)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("shape", sorted(SHAPES))
+def test_absorbed_not_finite(lib, dev, e4m3, shape):
+    """A NaN, or a score of +inf, among a token's keys makes out and lse NaN,
+    not the zeros and -inf of a token without keys; a score of -inf weighs
+    nothing.  Other tokens are as they would be without."""
+    T, H, k = SHAPES[shape]
+    rng = np.random.default_rng(31)
+    cache = Cache(rng, 3000, e4m3, dev)
+    q, qh = _bf(rng, (T, H, 576), dev)
+    q[:, :, 512 + 9], q[:, :, 512 + 11] = 1, -1
+    qh[:, :, 512 + 9], qh[:, :, 512 + 11] = 1, -1
+    cache.rope[0, 5] = float("nan")
+    if e4m3:
+        cache.scale[1] = float("nan")
+    else:
+        cache.latent[1, 7] = float("nan")
+    cache.rope[2, 9] = float("inf")
+    cache.rope[3, 11] = float("inf")          # a score of -inf
+    idx = np.stack([4 + rng.permutation(2996)[:k] for _ in range(T)])
+    kind = np.arange(T) % 5                   # 0: no such key; 1 to 4: the slot before it
+    for t in np.nonzero(kind)[0]:
+        idx[t, rng.integers(k)] = kind[t] - 1
+    for form, out, lse in _both_absorbed(lib, dev, cache, q, idx, 0.07):
+        out, lse = _host(out), _host(lse)
+        bad = (kind >= 1) & (kind <= 3)
+        assert np.isnan(out[bad]).all() and np.isnan(lse[bad]).all(), form
+        for t in np.nonzero(~bad)[0][:8]:
+            _check_token(f"{form} token {t}", cache, qh[t], idx[t][idx[t] > 3], 0.07, out[t], lse[t], heads=(0, H // 2, H - 1))
+
+
+@pytest.mark.parametrize("nq,nk", [(70, 333), (40, 4500)])      # one workgroup to a block, and several
+def test_expanded_not_finite(lib, dev, nq, nk):
+    """The same for the expanded form, query by query."""
+    rng = np.random.default_rng(32)
+    q, qh = _bf(rng, (nq, 2, 192), dev)
+    q[:, :, 128 + 5], q[:, :, 128 + 7] = 1, -1
+    qh[:, :, 128 + 5], qh[:, :, 128 + 7] = 1, -1
+    kv, kvh = _bf(rng, (nk, 2, 256), dev)
+    rope, rh = _bf(rng, (nk, 64), dev)
+    rope[2, 7] = float("inf")                       # a score of -inf
+    kv[nk - nq + 10, 0, 3] = float("nan")           # head 0, from query 10 on
+    rope[nk - nq + 20, 5] = float("inf")            # a score of +inf, from query 20 on
+    out, lse = lib.latent_attention_expanded(q, kv, rope, _i32([0, nq], dev), _i32([0, nk], dev), 0.1)
+    out, lse = _host(out), _host(lse)
+    for h, first in ((0, 10), (1, 20)):
+        assert np.isnan(out[first:, h]).all() and np.isnan(lse[first:, h]).all()
+        for i in (0, 5, first - 1):
+            at = np.setdiff1d(np.arange(lo.causal_keys(i, nq, nk)), [2])
+            a = lo.attend(qh[i, h], np.concatenate([kvh[at, h, :128], rh[at]], 1), kvh[at, h, 128:], 0.1)
+            assert lo.check("out", out[i, h], a.out, a.out_bound) is None
+            assert lo.check("lse", lse[i, h], a.lse, a.lse_bound) is None
