@@ -318,13 +318,20 @@ __device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], uint32_
 #pragma unroll
     for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
   top = max_of_4(top) * scale_log2;
-  if (__any(top > st.m + kLazy)) {
+  if (__any(top > st.m + kLazy || fabsf(st.m) > kFar)) {
     const float m = fmaxf(st.m, top);
     const float f = __builtin_amdgcn_exp2f(st.m - m);
     st.m = m;
     st.l *= f;
 #pragma unroll
     for (int cb = 0; cb < kColBlocks; ++cb) st.o[cb] *= f;
+    if (__any(fabsf(m) > kFar)) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[b][r] *= scale_log2;
+      scale_log2 = 1.0f;
+    }
   }
   // Weights in bf16 (the matrix cores' type): an unbiased half step of 2^-9 on
   // each, as large as the rounding of the result itself.  The sum keeps them in fp32.

@@ -198,12 +198,21 @@ constexpr float kLn2 = 0.69314718055994530942f;
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
 __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2; }
 
-// Initial reference maximum of a running softmax: finite, so that masked
-// scores (-inf) give weights of exactly 0 and never inf - inf.
-constexpr float kNoMax = -1e30f;
-// The running reference is moved only when a score passes it by more than
-// 2^kLazy: weights then reach at most 2^kLazy, and the accumulators are
+// Initial reference maximum of a running softmax: no finite score is below it, and
+// it is finite itself, so that masked scores (-inf) give weights of exactly 0 and
+// never inf - inf.
+constexpr float kNoMax = -3.40282347e38f;
+// The running reference is moved only when a score (log2 units) passes it by more than
+// kLazy: weights then reach at most 2^kLazy, and the accumulators are
 // rescaled a few times a row rather than at every tile.
 constexpr float kLazy = 8.0f;
+
+// A weight's exponent is the product s * scale less the reference, which is such a
+// product rounded.  One fused step leaves that rounding in the exponent: the same
+// for all keys of a row, so it does no harm up to kFar, where it is at most 1,
+// but at 2^31 it reaches 128, and weights overflow or vanish.  A tile whose
+// reference is beyond kFar has its products rounded first (and scale 1 after that), so that
+// the largest score's distance is exactly 0.
+constexpr float kFar = 16777216.0f;
 
 }  // namespace latent

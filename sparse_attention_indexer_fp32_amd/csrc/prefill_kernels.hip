@@ -386,7 +386,7 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
       top = fmaxf(top, s[kb][r]);
     }
   top = fmaxf(top, other_half(top, lane)) * scale_log2;
-  if (__any(top > st.m + kLazy)) {
+  if (__any(top > st.m + kLazy || fabsf(st.m) > kFar)) {
     const float m = fmaxf(st.m, top);
     const float f = __builtin_amdgcn_exp2f(st.m - m);
     st.m = m;
@@ -395,6 +395,13 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
     for (int cb = 0; cb < kColBlocks; ++cb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) st.o[cb][r] *= f;
+    if (__any(fabsf(m) > kFar)) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[kb][r] *= scale_log2;
+      scale_log2 = 1.0f;
+    }
   }
   // Weights in bf16 (the matrix cores' type): an unbiased half step of 2^-9 on
   // each, as large as the rounding of the result itself.  The sum keeps them in fp32.

@@ -809,3 +809,75 @@ def test_expanded_not_finite(lib, dev, nq, nk):
             a = lo.attend(qh[i, h], np.concatenate([kvh[at, h, :128], rh[at]], 1), kvh[at, h, 128:], 0.1)
             assert lo.check("out", out[i, h], a.out, a.out_bound) is None
             assert lo.check("lse", lse[i, h], a.lse, a.lse_bound) is None
+
+
+# ---- scores of any finite size ------------------------------------------------------------------------------
+
+def _size(t, h):
+    """Of a score's unit: powers of two up to 2^118, of both signs."""
+    a = (10, 22, 27, 31, 33, 40, 60, 100, 110, 118)[(t + 3 * h) % 10]
+    return (-1.0) ** (t + h) * 2.0 ** a
+
+
+def _check_largest(name, sizes, units, values, scale, out, lse):
+    """Rows of scores scale * size * unit, whole units apart: the largest score's
+    keys share all the weight.  out: their mean, rounded to bf16, as the weights
+    and their products with a scale are; lse: fp32."""
+    for at in np.ndindex(*sizes.shape):
+        z = sizes[at] * units[at[0]]
+        top = z == z.max()
+        want = values[at][top].mean(0)
+        size = np.abs(values[at][top]).mean(0)
+        assert lo.check(f"{name} {at} out", out[at], want, lo.U16 * np.abs(want) + (lo.U16 * 1.01 + 64 * lo.U32) * size) is None
+        want = scale * z.max() + np.log(top.sum())
+        # a product of the scale, its conversion to and from base 2, a logarithm, a sum
+        assert lo.check(f"{name} {at} lse", lse[at], want, 8 * lo.U32 * (abs(want) + abs(scale * z.max()) + 1)) is None
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("shape", sorted(SHAPES))
+def test_absorbed_scores_of_any_size(lib, dev, e4m3, shape):
+    """Scores whose distance from the largest cannot be told within fp32 of their
+    own size, or that all lie below any constant, still weigh at most 1."""
+    import torch
+    T, H, k = SHAPES[shape]
+    rng = np.random.default_rng(33)
+    cache = Cache(rng, 3000, e4m3, dev)
+    units = rng.integers(2, 200, 3000)
+    units[rng.permutation(3000)[:60]] = 200
+    units[rng.permutation(3000)[:60]] = 1
+    cache.rope[:, 5] = torch.from_numpy(units.astype(np.float32)).bfloat16().to(dev)
+    sizes = np.array([[_size(t, h) for h in range(H)] for t in range(T)])
+    q = torch.zeros((T, H, 576), dtype=torch.bfloat16, device=dev)
+    q[:, :, 512 + 5] = torch.from_numpy(sizes).to(dev).bfloat16()
+    idx = np.stack([rng.permutation(3000)[:k] for _ in range(T)])
+    few = min(T, 10)
+    for form, out, lse in _both_absorbed(lib, dev, cache, q, idx, 0.3):
+        out, lse = _host(out), _host(lse)
+        assert np.isfinite(out).all() and np.isfinite(lse).all(), form
+        for t in range(few):
+            for h in {0, 1, 2, H // 2, H - 1}:
+                _check_largest(f"{form} token {t} head {h}", sizes[t:t + 1, h], units[idx[t]][None], cache.c[idx[t]][None], 0.3,
+                               out[t:t + 1, h], lse[t:t + 1, h])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("nq,nk", [(70, 333), (40, 4500)])      # one workgroup to a block, and several
+def test_expanded_scores_of_any_size(lib, dev, nq, nk, causal):
+    import torch
+    rng = np.random.default_rng(34)
+    units = rng.integers(2, 200, nk)
+    units[rng.permutation(nk)[:nk // 40]] = 200
+    units[rng.permutation(nk)[:nk // 40]] = 1
+    kv, kvh = _bf(rng, (nk, 3, 256), dev)
+    rope = _bf(rng, (nk, 64), dev)[0]
+    rope[:, 5] = torch.from_numpy(units.astype(np.float32)).bfloat16().to(dev)
+    sizes = np.array([[_size(i, h) for h in range(3)] for i in range(nq)])
+    q = torch.zeros((nq, 3, 192), dtype=torch.bfloat16, device=dev)
+    q[:, :, 128 + 5] = torch.from_numpy(sizes).to(dev).bfloat16()
+    out, lse = lib.latent_attention_expanded(q, kv, rope, _i32([0, nq], dev), _i32([0, nk], dev), 0.3, causal=causal)
+    out, lse = _host(out), _host(lse)
+    for i in range(nq):
+        n = lo.causal_keys(i, nq, nk, causal)
+        for h in range(3):
+            _check_largest(f"query {i} head {h}", sizes[i:i + 1, h], units[None, :n], kvh[None, :n, h, 128:], 0.3, out[i:i + 1, h], lse[i:i + 1, h])
