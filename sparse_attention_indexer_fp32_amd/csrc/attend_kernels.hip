@@ -336,16 +336,18 @@ __device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], uint32_
   // Weights in bf16 (the matrix cores' type): an unbiased half step of 2^-9 on
   // each, as large as the rounding of the result itself.  The sum keeps them in fp32.
   bf16x8 p;
+  float sum = 0.f;                        // a tile at a time: few additions to a large number
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     f32x4 w;
 #pragma unroll
     for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], scale_log2, -st.m));
-    st.l += (w[0] + w[1]) + (w[2] + w[3]);
+    sum += (w[0] + w[1]) + (w[2] + w[3]);
     if (E4M3) w *= read_lds<f32x4>(scales + 64 * b + 16 * g);
 #pragma unroll
     for (int r = 0; r < 4; ++r) p[4 * b + r] = (__bf16)w[r];
   }
+  st.l += sum;
   const uint32_t value = (uint32_t)here(at.value + (int)lat);
   auto use = [&](int cb, bf16x8 cols) { st.o[cb] = mfma16(cols, p, st.o[cb]); };
   if constexpr (E4M3) {

@@ -404,17 +404,21 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
     }
   }
   // Weights in bf16 (the matrix cores' type): an unbiased half step of 2^-9 on
-  // each, as large as the rounding of the result itself.  The sum keeps them in fp32.
+  // each, as large as the rounding of the result itself.  The sum keeps them in
+  // fp32, a tile at a time: added to the running sum one by one, a long row's many
+  // small weights would each be rounded against it (131072 equal ones 3e-4 off).
   bf16x8 p[4];
+  float sum[2] = {};
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const float w = __builtin_amdgcn_exp2f(fmaf(s[kb][r], scale_log2, -st.m));
-      st.l += w;
+      sum[kb] += w;
       if (MASKED) s[kb][r] = w;
       p[2 * kb + ((r >> 2) & 1)][((r >> 3) << 2) + (r & 3)] = (__bf16)w;   // a step: rows 0..3 and 16..19 of each half
     }
+  st.l += sum[0] + sum[1];
   if (MASKED && values_not_finite(t, lane_here())) {
     add_values_one_by_one(st.o, s, t, limit, lane_here());
     return;
@@ -565,11 +569,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
       lds_barrier();              // every wave's rows are there, and nobody reads the other stage any more
       if (j0 + kKeys < end) queue(j0 + kKeys, nxt);
       if (j0 >= wave_most) return;
+      // (Split, the offsets are worked out for every tile: one that is kept does not fit the
+      // registers, and its reload waits for the rows on their way: 100 queries x 8 heads
+      // behind 60000 keys 101 us so, 94 like this.)
+      const TileReads at = SPLIT ? tile_reads(lane_here()) : reads;
       if (j0 + kKeys <= wave_least) {
-        attend_tile<false>(st, cur, reads, kKeys, scale_log2, lane);
+        attend_tile<false>(st, cur, at, kKeys, scale_log2, lane);
       } else {
         const int left = own_keys - (int)j0;
-        attend_tile<true>(st, cur, reads, left < 0 ? 0 : (left < kKeys ? left : kKeys), scale_log2, lane);
+        attend_tile<true>(st, cur, at, left < 0 ? 0 : (left < kKeys ? left : kKeys), scale_log2, lane);
       }
     };
     for (int64_t j0 = begin; j0 < end; j0 += 2 * kKeys) {

@@ -881,3 +881,26 @@ def test_expanded_scores_of_any_size(lib, dev, nq, nk, causal):
         n = lo.causal_keys(i, nq, nk, causal)
         for h in range(3):
             _check_largest(f"query {i} head {h}", sizes[i:i + 1, h], units[None, :n], kvh[None, :n, h, 128:], 0.3, out[i:i + 1, h], lse[i:i + 1, h])
+
+
+def test_expanded_many_keys_of_equal_weight(lib, dev):
+    """131072 keys of weight 0.7 after one of weight 1, one workgroup to a block.
+    The sum takes a tile of 64 keys at a time (32 to a lane), so 2048 additions
+    to the running sum and 32 within a tile, each off by at most half a step,
+    and 2 units for each weight; one addition a key would be off by 6e-4."""
+    import torch
+    K, H = 131072, 384
+    rng = np.random.default_rng(35)
+    q = torch.zeros((1, H, 192), dtype=torch.bfloat16, device=dev)
+    q[:, :, 128] = 1
+    row, rowh = _bf(rng, (1, H, 256), dev)
+    rope = torch.zeros((K, 64), dtype=torch.bfloat16, device=dev)
+    rope[1:, 0] = np.log(0.7)
+    other = float(rope[1, 0])
+    out, lse = lib.latent_attention_expanded(q, row.expand(K, H, 256), rope, _i32([0, 1], dev), _i32([0, K], dev), 1.0)
+    want = np.log(1 + (K - 1) * np.exp(other))
+    bound = (2048 + 32 + 4) * lo.U32 + 8 * lo.U32 * (1 + want)
+    assert lo.check("lse", _host(lse)[0], np.full(H, want), bound) is None
+    # every value is its head's row: weights and result rounded to bf16, the weighted sum of a tile at a time
+    size = np.abs(rowh[0, :, 128:])
+    assert lo.check("out", _host(out)[0], rowh[0, :, 128:], (2.02 * lo.U16 + 2 * K // 16 * lo.U32) * size) is None
