@@ -253,3 +253,90 @@ def test_binding_refuses_before_any_call():
         binding._outputs(z(2, 4, 511), None, 2, 4, 512, cpu)
     with pytest.raises(ValueError):
         binding._outputs(None, z(2, 4), 2, 4, 512, cpu)
+
+
+# ---- the binding's checks, each by its one defect ------------------------------------------------------
+
+ON_CPU = -1   # the device number of CPU tensors
+
+
+def _zeros(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+@pytest.fixture(scope="module")
+def binding():
+    from sparse_attention_indexer_fp32_amd import latent
+    latent._modules()
+    return latent
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("slots", [0, 1, 4])
+def test_binding_takes_a_cache(binding, e4m3, slots):
+    """A cache as it should be, and as a view of a wider buffer, is taken with its strides."""
+    latent = _zeros(slots, 512, dtype=torch.uint8 if e4m3 else torch.bfloat16)
+    scale = _zeros(slots, dtype=torch.float32) if e4m3 else None
+    rope = _zeros(slots, 64)
+    args, n = binding._cache(latent, rope, scale, ON_CPU)
+    assert n == slots and args[1] == 512 and args[3] == 64 and args[5] == int(e4m3)
+    wide = _zeros(slots, 640, dtype=latent.dtype)
+    args, n = binding._cache(wide[:, :512], _zeros(slots, 128)[:, 64:], scale, ON_CPU)
+    assert n == slots and (args[1], args[3]) == ((640, 128) if slots > 1 else (512, 64))
+
+
+@pytest.mark.parametrize("name,match", [
+    ("narrow", "latent must be"), ("transposed", "latent must be"), ("flat", "latent must be"), ("elsewhere", "latent must be"),
+    ("rope_rows", "rope must be"), ("rope_width", "rope must be"), ("rope_type", "rope must be"), ("rope_transposed", "rope must be"),
+    ("latent_type", "latent must be bfloat16"), ("codes_without_scale", "latent must be bfloat16"), ("scale_of_bf16", "an 8-bit cache"),
+    ("scale_rows", "an 8-bit cache"), ("scale_type", "an 8-bit cache"), ("scale_strided", "an 8-bit cache"),
+])
+def test_binding_refuses_a_cache(binding, name, match):
+    codes, f32 = _zeros(4, 512, dtype=torch.uint8), torch.float32
+    latent, rope, scale, at = {
+        "narrow": (_zeros(4, 500), _zeros(4, 64), None, ON_CPU),
+        "transposed": (_zeros(512, 4).T, _zeros(4, 64), None, ON_CPU),
+        "flat": (_zeros(512), _zeros(4, 64), None, ON_CPU),
+        "elsewhere": (_zeros(4, 512), _zeros(4, 64), None, 0),
+        "rope_rows": (_zeros(4, 512), _zeros(3, 64), None, ON_CPU),
+        "rope_width": (_zeros(4, 512), _zeros(4, 65), None, ON_CPU),
+        "rope_type": (_zeros(4, 512), _zeros(4, 64, dtype=f32), None, ON_CPU),
+        "rope_transposed": (_zeros(4, 512), _zeros(64, 4).T, None, ON_CPU),
+        "latent_type": (_zeros(4, 512, dtype=torch.float16), _zeros(4, 64), None, ON_CPU),
+        "codes_without_scale": (codes, _zeros(4, 64), None, ON_CPU),
+        "scale_of_bf16": (_zeros(4, 512), _zeros(4, 64), _zeros(4, dtype=f32), ON_CPU),
+        "scale_rows": (codes, _zeros(4, 64), _zeros(3, dtype=f32), ON_CPU),
+        "scale_type": (codes, _zeros(4, 64), _zeros(4), ON_CPU),
+        "scale_strided": (codes, _zeros(4, 64), _zeros(8, dtype=f32)[::2], ON_CPU),
+    }[name]
+    with pytest.raises(ValueError, match=match):
+        binding._cache(latent, rope, scale, at)
+
+
+def test_binding_checks_queries_and_outputs(binding):
+    f32 = torch.float32
+    assert binding._queries(_zeros(2, 5, 600)[:, 1:, :576], 576)[:2] == (2, 4)
+    assert binding._queries(_zeros(2, 4, 576), 576)[2][1:] == (4 * 576, 576)
+    for bad in (_zeros(2, 4, 570), _zeros(2, 576), _zeros(2, 4, 576, dtype=f32), _zeros(576, 4, 2).permute(2, 1, 0)):
+        with pytest.raises(ValueError, match="q must be"):
+            binding._queries(bad, 576)
+    good = (_zeros(2, 4, 512), _zeros(2, 4, dtype=f32))
+    binding._outputs(*good, 2, 4, 512, ON_CPU)
+    binding._outputs(None, None, 2, 4, 512, ON_CPU)
+    for bad in (_zeros(2, 4, 511), _zeros(2, 3, 512), _zeros(2, 4, 512, dtype=f32), _zeros(4, 2, 512).transpose(0, 1)):
+        with pytest.raises(ValueError, match="out must be"):
+            binding._outputs(bad, good[1], 2, 4, 512, ON_CPU)
+    for bad in (_zeros(2, 4), _zeros(2, 5, dtype=f32), _zeros(4, 2, dtype=f32).T):
+        with pytest.raises(ValueError, match="lse must be"):
+            binding._outputs(good[0], bad, 2, 4, 512, ON_CPU)
+    with pytest.raises(ValueError, match="out must be"):
+        binding._outputs(*good, 2, 4, 512, 0)
+    rows = (_zeros(3, 512), _zeros(3, 64))
+    binding._load_outputs(*rows, 3, ON_CPU)
+    for bad in ((_zeros(3, 500), rows[1]), (rows[0], _zeros(2, 64)), (rows[0].float(), rows[1])):
+        with pytest.raises(ValueError, match="must be a contiguous bfloat16"):
+            binding._load_outputs(*bad, 3, ON_CPU)
+    binding._int32("x", _zeros(3, dtype=torch.int32), (3,), ON_CPU)
+    for bad in (_zeros(3, dtype=torch.int64), _zeros(4, dtype=torch.int32), _zeros(6, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError, match="x must be a contiguous int32"):
+            binding._int32("x", bad, (3,), ON_CPU)
