@@ -202,8 +202,9 @@ topk_status_t latent_attention_paged(const uint16_t* q, int64_t q_token_stride, 
                                      int32_t num_heads, int32_t num_requests, int64_t pages_per_row,
                                      int64_t num_slots);
 
-/* Bytes of workspace for num_tokens tokens of num_heads heads that attend at
- * most `keys` keys each (on the current device). */
+/* Bytes of workspace for up to num_tokens tokens of num_heads heads that attend
+ * up to `keys` keys each (on the current device): it grows with both, so that of a
+ * step's largest call serves the smaller ones. */
 topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, int64_t keys, size_t* bytes);
 
 /*
@@ -237,7 +238,7 @@ topk_status_t latent_attention_expanded(const uint16_t* q, int64_t q_token_strid
                                         float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream,
                                         int32_t num_tokens, int64_t num_kv, int32_t num_heads, int32_t num_requests);
 
-/* Bytes of workspace of a call with these sizes (on the current device). */
+/* Bytes of workspace of a call with these sizes or smaller ones (on the current device). */
 topk_status_t latent_attention_expanded_workspace(int32_t num_tokens, int32_t num_heads, int64_t num_kv,
                                                   int32_t num_requests, size_t* bytes);
 

@@ -93,6 +93,24 @@ float scale_log2(float softmax_scale) {
   return softmax_scale == 0.f ? 0x1p-100f : softmax_scale * 1.44269504088896340736f;
 }
 
+// Tiles of a token that attends `keys` keys, and one more: an upper bound for what the kernel counts.
+int64_t bound_tiles(int64_t keys) { return keys / latent::kTileKeys + (keys % latent::kTileKeys != 0) + 1; }
+
+// The most workgroups that share so many tokens' tiles: it grows with both.  One takes
+// a CU's LDS, and kShareTiles tiles or more: one token of 64 tiles x 128 heads
+// took 27.8 us at one tile to a workgroup, 22.3 at two and 21.9 at four; 4 tokens
+// x 64 heads 31.6, 26.6 and 25.3.
+int most_wgs(int cus, int32_t num_tokens, int64_t blocks, int64_t tiles) {
+  const int64_t wgs = cus / blocks, share = latent::kShareTiles;
+  const int64_t most = tiles > share * cus ? wgs : num_tokens * tiles / share;
+  return most < 1 || wgs < 1 ? 1 : (int)(wgs < most ? wgs : most);
+}
+
+int64_t head_blocks(int32_t num_heads) {
+  const int heads = latent::attend_heads(num_heads);
+  return ((int64_t)num_heads + heads - 1) / heads;
+}
+
 // Workgroups that share the tiles of a launch of absorbed attention, or 0 for one
 // workgroup per token.  Not split, two workgroups run on a CU at a time, and the
 // last round of them may leave most CUs idle: split is what leaves more than a
@@ -103,22 +121,14 @@ float scale_log2(float softmax_scale) {
 // 222, 2048 tokens 689 and 817), and as fast otherwise (512 tokens 173 and 172,
 // 2048 tokens 669 and 656), so all of them are; with 16 heads they are not
 // (1024 tokens 336 and 331, 8-bit 361 and 330).
-// A workgroup takes kShareTiles tiles or more: one token of 64 tiles x 128 heads
-// took 27.8 us at one tile to a workgroup, 22.3 at two and 21.9 at four; 4 tokens
-// x 64 heads 31.6, 26.6 and 25.3.
 int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, bool paged, int32_t num_requests) {
   if (paged && (num_tokens > latent::kPlanTokens || num_requests > 65535)) return 0;
-  const int heads = latent::attend_heads(num_heads);
-  const int64_t blocks = (num_heads + heads - 1) / heads;
-  const int64_t token_tiles = (keys + latent::kTileKeys - 1) / latent::kTileKeys + 1;
-  if (token_tiles > (int64_t)INT32_MAX / num_tokens) return 0;   // the plan counts tiles in 32 bits
+  const int64_t blocks = head_blocks(num_heads), tiles = bound_tiles(keys);
+  if (tiles > (int64_t)INT32_MAX / num_tokens) return 0;         // the plan counts tiles in 32 bits
   const int64_t items = num_tokens * blocks, round = 2 * (int64_t)cus;
   const int64_t rounds = (items + round - 1) / round;
   if (latent::attend_waves(num_heads) != 2 && 3 * items >= 2 * rounds * round) return 0;
-  int64_t wgs = cus / blocks;                                    // one takes a CU's LDS
-  const int64_t most = num_tokens * token_tiles / latent::kShareTiles;
-  if (wgs > most) wgs = most;
-  return wgs < 1 ? 1 : (int)wgs;
+  return most_wgs(cus, num_tokens, blocks, tiles);
 }
 
 // The same for the expanded form: workgroups that share all units' tiles, or 0
@@ -129,9 +139,10 @@ int split_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t keys, bool
 // x 64 behind 2000 57 and 66, behind 1000 54 and 43; 1500 x 32 behind 6000 266
 // and 266, 2048 x 32 behind 8000 427 and 390: shares of a head read
 // different keys at a time, blocks of a head the same ones out of L2).
+constexpr int64_t kSplitKeys = 32 * 64;
 int prefill_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t num_kv, int32_t num_requests) {
   const int64_t units = latent::prefill_blocks(num_tokens, num_requests) * num_heads, round = 2 * (int64_t)cus;
-  const bool pays = 4 * units < 3 * round && num_kv >= 32 * 64 * (int64_t)num_requests;
+  const bool pays = 4 * units < 3 * round && num_kv >= kSplitKeys * num_requests;
   return num_requests <= latent::kPlanRequests && pays ? (int)round : 0;
 }
 
@@ -315,8 +326,9 @@ topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, 
   int cus = 0;
   const topk_status_t st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
-  const int wgs = split_wgs(cus, num_tokens, num_heads, keys, false, 0);   // the same for whole sequences, or 0
-  if (wgs > 0) *bytes = latent::split_layout(num_tokens, num_heads, wgs).total();
+  // Also of fewer tokens and keys, which may be split where these are not.
+  const int wgs = most_wgs(cus, num_tokens, head_blocks(num_heads), bound_tiles(keys));
+  *bytes = latent::split_layout(num_tokens, num_heads, wgs).total();
   return TOPK_SUCCESS;
 }
 
@@ -397,8 +409,8 @@ topk_status_t latent_attention_expanded_workspace(int32_t num_tokens, int32_t nu
   int cus = 0;
   const topk_status_t st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
-  const int wgs = prefill_wgs(cus, num_tokens, num_heads, num_kv, num_requests);
-  if (wgs > 0) *bytes = latent::prefill_split_layout(num_tokens, num_heads, num_requests, wgs).total();
+  // Also of smaller calls, which may be split where this one is not.
+  if (num_kv >= kSplitKeys) *bytes = latent::prefill_split_layout(num_tokens, num_heads, num_requests, 2 * cus).total();
   return TOPK_SUCCESS;
 }
 

@@ -904,3 +904,39 @@ def test_expanded_many_keys_of_equal_weight(lib, dev):
     # every value is its head's row: weights and result rounded to bf16, the weighted sum of a tile at a time
     size = np.abs(rowh[0, :, 128:])
     assert lo.check("out", _host(out)[0], rowh[0, :, 128:], (2.02 * lo.U16 + 2 * K // 16 * lo.U32) * size) is None
+
+
+def test_workspace_serves_smaller_calls(lib, dev):
+    """A workspace of the size that is said for a step's largest call serves every
+    call with fewer tokens and keys, also those that are split where the
+    largest is not."""
+    import ctypes
+
+    import torch
+    n = ctypes.c_size_t(0)
+    L = lib.load()
+    cache = Cache(np.random.default_rng(36), 64, False, dev)
+    x = torch.zeros((600, 64, 576), dtype=torch.bfloat16, device=dev)
+    idx = torch.zeros((600, 2048), dtype=torch.int32, device=dev)
+    out = torch.empty((600, 64, 512), dtype=torch.bfloat16, device=dev)
+    for H in (16, 32, 64):
+        for T, k in ((512, 2048), (600, 700)):
+            assert L.latent_attention_workspace(T, H, k, ctypes.byref(n)) == 0
+            ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+            for t, kk in ((T, k), (300, k), (300, 64), (64, k), (5, 2 * k // 3), (1, k), (1, 1)):
+                st = L.latent_attention(x.data_ptr(), 64 * 576, 576, cache.latent.data_ptr(), 512, cache.rope.data_ptr(), 64, None, 0,
+                                        idx.data_ptr(), 0.1, out.data_ptr(), None, ws.data_ptr(), n.value,
+                                        torch.cuda.current_stream().cuda_stream, t, H, kk, 64)
+                assert st == 0, (H, T, k, t, kk, lib.topk_last_error())
+            torch.cuda.synchronize()
+    q_starts, kv_starts = _i32([0, 1, 2], dev), _i32([0, 2048, 6000], dev)
+    kv = torch.zeros((6000, 64, 256), dtype=torch.bfloat16, device=dev)
+    rope = torch.zeros((6000, 64), dtype=torch.bfloat16, device=dev)
+    assert L.latent_attention_expanded_workspace(600, 64, 6000, 3, ctypes.byref(n)) == 0
+    ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    for t, K, H, B in ((2, 6000, 64, 2), (2, 6000, 4, 2), (1, 2048, 64, 1), (600, 6000, 5, 2), (1, 1, 1, 1)):
+        st = L.latent_attention_expanded(x.data_ptr(), 64 * 576, 192, kv.data_ptr(), 64 * 256, 256, rope.data_ptr(), 64, q_starts.data_ptr(),
+                                         kv_starts.data_ptr(), 0.1, 1, out.data_ptr(), None, ws.data_ptr(), n.value,
+                                         torch.cuda.current_stream().cuda_stream, t, K, H, B)
+        assert st == 0, (t, K, H, B, lib.topk_last_error())
+    torch.cuda.synchronize()
