@@ -77,6 +77,8 @@ def _modules() -> None:
 @contextlib.contextmanager
 def _on(dev, stream):
     """The tensors' device made current and, for allocations, the call's stream."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream must be one of {dev}, the tensors' device")
     with torch.cuda.device(dev):
         if stream is None:
             yield

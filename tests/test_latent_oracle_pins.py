@@ -340,3 +340,14 @@ def test_binding_checks_queries_and_outputs(binding):
     for bad in (_zeros(3, dtype=torch.int64), _zeros(4, dtype=torch.int32), _zeros(6, dtype=torch.int32)[::2]):
         with pytest.raises(ValueError, match="x must be a contiguous int32"):
             binding._int32("x", bad, (3,), ON_CPU)
+
+
+def test_binding_refuses_a_stream_of_another_device(binding):
+    """A kernel launched on another device's stream would read memory that is not there."""
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    with pytest.raises(ValueError, match="stream"):
+        with binding._on(torch.device("cuda", 0), Stream()):
+            raise AssertionError("the call is on its way")
