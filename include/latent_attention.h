@@ -31,7 +31,10 @@
  * reads, but for the page table that is updated in place.  Status codes and topk_last_error() are
  * topk_transform.h's.  Errors of every call: TOPK_ERROR_INVALID_VALUE for a
  * negative size, a required pointer that is NULL, a page size that is not a
- * power of two, a misaligned pointer or stride; TOPK_ERROR_UNSUPPORTED on a
+ * power of two, a misaligned pointer or stride, sizes that need 2^32 threads or more
+ * (2^29 loaded rows; in the absorbed form 2^26 tokens of up to 16 heads, or 2^24
+ * tokens times blocks of 64 heads; in the expanded form 2^24 heads times blocks of up
+ * to 128 queries); TOPK_ERROR_UNSUPPORTED on a
  * device that is not gfx950; TOPK_ERROR_LAUNCH.  On error nothing was queued.
  *
  * These entry points are additions: they leave topk_abi_version() as it is.

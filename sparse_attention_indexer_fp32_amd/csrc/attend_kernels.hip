@@ -776,9 +776,7 @@ int ceil_div(int a, int b) { return (int)(((int64_t)a + b - 1) / b); }
 template <int NW, int RINGS, bool E4M3>
 hipError_t launch(const AttendArgs& a, hipStream_t stream) {
   const int64_t shares = ceil_div(a.wgs > 0 ? a.wgs : a.num_tokens, 8);
-  const int64_t x = shares * 8 * ceil_div(a.num_heads, kHeads * NW);
-  if (x > (int64_t)INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)x), block(64 * NW * RINGS);
+  const dim3 grid((unsigned)(shares * 8 * ceil_div(a.num_heads, kHeads * NW))), block(64 * NW * RINGS);
   constexpr int kLds = Lds<NW, RINGS, E4M3>::kBytes;
   static_assert(sizeof(SplitPlan) <= (size_t)kLds, "the plan is made where the rows go");
   if (a.indices)
@@ -815,6 +813,14 @@ int attend_waves(int num_heads) {
 }
 
 int attend_heads(int num_heads) { return kHeads * attend_waves(num_heads); }
+
+int64_t attend_threads(int num_tokens, int num_heads) {
+  const int64_t wgs = (int64_t)ceil_div(num_tokens, 8) * 8 * ceil_div(num_heads, attend_heads(num_heads));
+  if (wgs > kMaxThreads) return wgs;
+  const int64_t own = wgs * 64 * attend_waves(num_heads);
+  const int64_t join = (int64_t)num_tokens * 64 * kJoinWaves;   // of a split launch: with 17 to 32 heads for any number of tokens
+  return attend_waves(num_heads) == 2 && join > own ? join : own;
+}
 
 SplitLayout split_layout(int num_tokens, int num_heads, int wgs) {
   const int nw = attend_waves(num_heads);

@@ -208,7 +208,7 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 template <bool E4M3>
 __global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * (kStoreThreads / 64) + (threadIdx.x >> 6);
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kStoreThreads / 64) + (threadIdx.x >> 6);
   if (t >= a.num_tokens) return;
   // all that depends on nothing is loaded first; only the angles wait for a load
   const int64_t slot = a.slot_map[t], pos = a.cos_sin ? a.positions[t] : 0;
@@ -388,7 +388,8 @@ hipError_t launch_append_plan(const PlanArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_cache_store(const StoreArgs& a, bool e4m3, hipStream_t stream) {
-  const dim3 grid((unsigned)ceil_div(a.num_tokens, kStoreThreads / 64));
+  const int64_t wgs = ceil_div(a.num_tokens, kStoreThreads / 64), most = kMaxThreads / kStoreThreads;
+  const dim3 grid((unsigned)(wgs < most ? wgs : most), (unsigned)ceil_div(wgs, most));
   if (e4m3)
     hipLaunchKernelGGL(store_kernel<true>, grid, dim3(kStoreThreads), 0, stream, a);
   else
@@ -396,8 +397,10 @@ hipError_t launch_cache_store(const StoreArgs& a, bool e4m3, hipStream_t stream)
   return hipGetLastError();
 }
 
+int64_t load_threads(int64_t num_rows) { return ceil_div(num_rows, (kLoadThreads / 64) * kLoadRows) * kLoadThreads; }
+
 hipError_t launch_cache_load(const LoadArgs& a, bool e4m3, hipStream_t stream) {
-  const dim3 grid((unsigned)ceil_div(a.num_rows, (kLoadThreads / 64) * kLoadRows)), block(kLoadThreads);
+  const dim3 grid((unsigned)(load_threads(a.num_rows) / kLoadThreads)), block(kLoadThreads);
   if (a.slots) {
     if (e4m3)
       hipLaunchKernelGGL((load_kernel<true, false>), grid, block, 0, stream, a);

@@ -161,6 +161,8 @@ topk_status_t check_queries(const uint16_t* q, int64_t q_token_stride, int64_t q
 // The launch of an absorbed call whose arguments hold; a's workspace from the caller's.
 topk_status_t attend(latent::AttendArgs& a, int64_t keys, bool e4m3, void* workspace, size_t workspace_bytes,
                      hipStream_t stream) {
+  if (latent::attend_threads(a.num_tokens, a.num_heads) > latent::kMaxThreads)
+    return invalid("more tokens and heads than a launch has threads for");
   int cus = 0;
   const topk_status_t st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
@@ -273,6 +275,7 @@ topk_status_t latent_cache_load(const int32_t* slots, const void* latent, int64_
   topk_status_t st = check_cache(latent, latent_stride, rope, rope_stride, scale, cache_type, num_slots, &a.cache);
   if (st != TOPK_SUCCESS) return st;
   if (num_rows < 0 || num_rows > (int64_t)INT32_MAX) return invalid("num_rows must be in [0, 2^31)");
+  if (latent::load_threads(num_rows) > latent::kMaxThreads) return invalid("more rows than a launch has threads for");
   if (num_rows == 0) return TOPK_SUCCESS;
   if (!slots || !out_latent || !out_rope) return invalid("slots, out_latent and out_rope must be non-null");
   if (!aligned(out_latent) || !aligned(out_rope)) return invalid("out_latent and out_rope must start on 16-byte boundaries");
@@ -299,6 +302,7 @@ topk_status_t latent_cache_load_paged(const int32_t* page_table, const int32_t* 
   a.log2_page = log2_of(page_size);
   if (a.log2_page < 0) return invalid("page_size must be a power of two");
   if (num_rows < 0 || num_rows > (int64_t)INT32_MAX) return invalid("num_rows must be in [0, 2^31)");
+  if (latent::load_threads(num_rows) > latent::kMaxThreads) return invalid("more rows than a launch has threads for");
   if (num_requests < 0 || pages_per_row < 0) return invalid("num_requests and pages_per_row must be >= 0");
   if (num_rows == 0 || num_requests == 0) return TOPK_SUCCESS;
   if (!kv_starts || !out_latent || !out_rope) return invalid("kv_starts, out_latent and out_rope must be non-null");
@@ -430,6 +434,8 @@ topk_status_t latent_attention_expanded(const uint16_t* q, int64_t q_token_strid
   if (!q_starts || !kv_starts) return invalid("q_starts and kv_starts must be non-null");
   if (num_kv > 0 && (!kv_up || !rope)) return invalid("kv_up and rope must be non-null when num_kv > 0");
   if (num_heads > 65535) return invalid("num_heads must be at most 65535");
+  if (latent::prefill_threads(num_tokens, num_heads, num_requests) > latent::kMaxThreads)
+    return invalid("more tokens, requests and heads than a launch has threads for");
   if (kv_token_stride < 0 || kv_head_stride < 0 || (num_heads > 1 && kv_head_stride < 2 * LATENT_HEAD_DIM) ||
       rope_stride < LATENT_ROPE_DIM)
     return invalid("kv_up's heads or rope's rows overlap, or a stride is negative");

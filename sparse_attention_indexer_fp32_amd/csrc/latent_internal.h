@@ -15,6 +15,10 @@ constexpr int kRope = LATENT_ROPE_DIM;
 constexpr int kQuery = kLatent + kRope;
 constexpr int kHead = LATENT_HEAD_DIM;
 
+// Threads of a launch along x: the hardware counts them in 32 bits, and what is
+// beyond is cut off without an error.
+constexpr int64_t kMaxThreads = UINT32_MAX;
+
 // A paged cache as the kernels see it; strides in bytes.
 struct Cache {
   const char* latent;
@@ -76,6 +80,7 @@ struct LoadArgs {
   int32_t num_requests;
   int32_t log2_page;
 };
+int64_t load_threads(int64_t num_rows);
 hipError_t launch_cache_load(const LoadArgs& a, bool e4m3, hipStream_t stream);
 
 // Absorbed form.  Tokens' keys are cut in tiles of kTileKeys.  Split: `wgs`
@@ -119,6 +124,7 @@ struct SplitLayout {
   size_t total() const { return out_bytes + ml_bytes + rec_bytes; }
 };
 SplitLayout split_layout(int num_tokens, int num_heads, int wgs);
+int64_t attend_threads(int num_tokens, int num_heads);     // the most of any launch of the call
 hipError_t launch_attend(const AttendArgs& a, bool e4m3, hipStream_t stream);
 
 // Expanded form.
@@ -150,6 +156,7 @@ struct PrefillArgs {
 };
 int64_t prefill_blocks(int num_tokens, int num_requests);   // of one head, at most
 SplitLayout prefill_split_layout(int num_tokens, int num_heads, int num_requests, int wgs);
+int64_t prefill_threads(int num_tokens, int num_heads, int num_requests);
 hipError_t launch_prefill(const PrefillArgs& a, hipStream_t stream);
 
 }  // namespace latent

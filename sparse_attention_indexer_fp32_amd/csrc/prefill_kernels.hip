@@ -688,6 +688,10 @@ int64_t prefill_blocks(int num_tokens, int num_requests) {
   return num_tokens / kRows + (num_requests < num_tokens ? num_requests : num_tokens);
 }
 
+int64_t prefill_threads(int num_tokens, int num_heads, int num_requests) {
+  return (prefill_blocks(num_tokens, num_requests) * num_heads + 7) / 8 * 8 * 64 * kWaves;
+}
+
 SplitLayout prefill_split_layout(int num_tokens, int num_heads, int num_requests, int wgs) {
   const size_t parts = (size_t)2 * wgs * kRows;
   SplitLayout s;
@@ -700,7 +704,6 @@ SplitLayout prefill_split_layout(int num_tokens, int num_heads, int num_requests
 hipError_t launch_prefill(const PrefillArgs& a, hipStream_t stream) {
   const int64_t blocks = prefill_blocks(a.num_tokens, a.num_requests);
   const int64_t grid = ((a.wgs > 0 ? a.wgs : blocks * a.num_heads) + 7) / 8 * 8;
-  if (grid > (int64_t)INT32_MAX) return hipErrorInvalidValue;
   if (a.wgs == 0) {
     hipLaunchKernelGGL(prefill_kernel<false>, dim3((unsigned)grid), dim3(64 * kWaves), 0, stream, a, blocks);
     return hipGetLastError();

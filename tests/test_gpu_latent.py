@@ -940,3 +940,28 @@ def test_workspace_serves_smaller_calls(lib, dev):
                                          torch.cuda.current_stream().cuda_stream, t, K, H, B)
         assert st == 0, (t, K, H, B, lib.topk_last_error())
     torch.cuda.synchronize()
+
+
+def test_store_more_tokens_than_a_launch_has_threads_for(lib, dev):
+    """2^26 tokens, a wave each: 2^32 threads.  All but the ends are padding."""
+    import torch
+    T, ends = 2 ** 26 + 5, [0, 1, 2 ** 25 - 1, 2 ** 25, 2 ** 26 - 1, 2 ** 26, 2 ** 26 + 4]
+    if torch.cuda.mem_get_info()[0] < 90e9:
+        pytest.skip("needs 90 GB")
+    rng = np.random.default_rng(37)
+    small, _ = _bf(rng, (len(ends), 576), dev)
+    at = torch.tensor(ends, device=dev)
+    kv = torch.empty((T, 576), dtype=torch.bfloat16, device=dev)
+    kv[at] = small
+    slot_map = torch.full((T,), -1, dtype=torch.int32, device=dev)
+    slot_map[at] = torch.arange(len(ends), dtype=torch.int32, device=dev)
+    positions = torch.zeros(T, dtype=torch.int32, device=dev)
+    positions[at] = torch.arange(len(ends), dtype=torch.int32, device=dev)
+    cos_sin = torch.randn((len(ends), 64), device=dev)
+    whole, few = ([torch.zeros((len(ends) + 1, n), dtype=torch.bfloat16, device=dev) for n in (512, 64)] for _ in range(2))
+    lib.latent_cache_store(kv, slot_map, *whole, positions=positions, cos_sin=cos_sin)
+    lib.latent_cache_store(small, slot_map[at], *few, positions=positions[at], cos_sin=cos_sin)
+    torch.cuda.synchronize()
+    assert torch.equal(whole[0], few[0]) and torch.equal(whole[1], few[1]) and bool(few[0][:-1].any(1).all())
+    del kv, slot_map, positions
+    torch.cuda.empty_cache()

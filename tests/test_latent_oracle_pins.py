@@ -351,3 +351,14 @@ def test_binding_refuses_a_stream_of_another_device(binding):
     with pytest.raises(ValueError, match="stream"):
         with binding._on(torch.device("cuda", 0), Stream()):
             raise AssertionError("the call is on its way")
+
+
+@pytest.mark.parametrize("call,kw", [
+    (_load, dict(rows=2 ** 29)), (_load_paged, dict(rows=2 ** 31 - 1)),
+    (_attention, dict(T=2 ** 26, H=16)), (_attention, dict(T=2 ** 26, H=1)), (_attention, dict(T=2 ** 24, H=32)),
+    (_attention, dict(T=2 ** 24, H=33)), (_attention, dict(T=2 ** 20, H=1024)), (_attention, dict(T=2 ** 31 - 1, H=2 ** 31 - 1)),
+    (_paged, dict(T=2 ** 26, H=7)), (_expanded, dict(T=2 ** 20, B=2 ** 20, H=16)), (_expanded, dict(T=2 ** 31 - 1, H=128)),
+])
+def test_launches_of_too_many_threads_are_refused(lib, call, kw):
+    """2^32 threads and more would be cut off without an error."""
+    assert call(lib, **kw) == 1 and "threads" in topk.topk_last_error()
