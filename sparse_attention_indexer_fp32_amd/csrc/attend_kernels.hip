@@ -35,14 +35,15 @@
 //
 // Measured (MI355X): 1024 tokens x 128 heads x 2048 selected bf16 slots of a
 // 65536-token cache 628-720 us over several cards, 810-930 TFLOP/s: the matrix
-// cores are busy 44 % of the time at the 1.96 GHz they clock to, LDS 45 %, and
-// the vector instructions take 44 %, which the two waves of a SIMD hardly get to
-// overlap with the matrix ones.  8-bit rows 790-830 us: widening them makes that
-// 71 %.  32 heads over 64 whole sequences of 4K to 64K bf16 tokens: 422 us, 6.1
-// TB/s of rows.  64 tokens x 64 heads x 2048 8-bit slots 44 + 9 us, of which the
+// cores are busy 42 % of the time at the 1.96 GHz they clock to, LDS 44 %, and
+// the vector instructions take 43 %, which the two waves of a SIMD hardly get to
+// overlap with the matrix ones.  8-bit rows 764-830 us: widening them makes that
+// 70 %.  With 64, 32 and 16 heads bf16 375, 332 and 273 us, 8-bit 427, 341 and 330: two
+// rings fill a CU whatever the heads, so few heads are few waves.  32 heads over 64
+// whole sequences of 4K to 64K bf16 tokens: 417-437 us, 6.1 TB/s of rows; 8-bit 351.
+// 64 tokens x 64 heads x 2048 8-bit slots 43-45 + 9 us, of which the
 // rows are 19 us of traffic and writing and joining 256 parts of 128 KB about 18.
-// One token x 32 heads x 2048 slots 12 + 4 us: a launch whose instructions have to
-// be fetched takes 10.5 us for a single tile.
+// One token x 32 heads x 2048 slots 12-13 + 4 us, one tile 10.6 + 4.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -333,7 +334,7 @@ __device__ __forceinline__ void weigh_tile(HeadState& st, f32x4 (&s)[2], uint32_
       scale_log2 = 1.0f;
     }
   }
-  // Weights in bf16 (the matrix cores' type): an unbiased half step of 2^-9 on
+  // Weights in bf16 (the matrix cores' type): an unbiased rounding of at most 2^-8 on
   // each, as large as the rounding of the result itself.  The sum keeps them in fp32.
   bf16x8 p;
   float sum = 0.f;                        // a tile at a time: few additions to a large number

@@ -172,8 +172,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
 // magnitude are wave reductions, the rotation's partner element comes from
 // another lane.  Nothing passes through LDS.
 // Measured (MI355X): 16000 tokens into 8-bit slots 10.2 us, 29 MB read and stored (6
-// us at a large copy's rate): vector instructions, about 200 a token, and the two
-// loads in turn.  (Reductions by lane permutes through LDS and eight divisions took
+// us at a large copy's rate), into bf16 ones 9.5, 37 MB (7.5): vector instructions,
+// about 200 a token in 8 bits, and the two loads in turn.  (Reductions by lane permutes through LDS and eight divisions took
 // 12.7 us.)  64 tokens 3.0 us: a launch and two loads in turn (position, then angles).
 constexpr int kStoreThreads = 256;
 
@@ -265,8 +265,9 @@ __global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
                                                                 : amax / 448.0f;
   if (lane == 0) a.scale[slot] = scale;
   // y / scale, at most 448 and a rounding, which E4M3 rounds back to 448.  The
-  // quotient by the reciprocal is corrected by its remainder, which rounds it as a
-  // division does, unless the remainder leaves the normal numbers (or scale is NaN).
+  // quotient by the reciprocal is corrected by its remainder (Markstein's step), which
+  // rounds it as a division does, unless the remainder leaves the normal numbers (or
+  // scale is NaN).
   if (scale > 0x1p-60f) {
     const float inv = 1.0f / scale;
 #pragma unroll
@@ -292,8 +293,8 @@ __global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
 // of each (all rows' loads are issued before the first store), and 16 bytes of
 // rotary key of one row.  By page table, the wave finds the request of its
 // rows by counting the starts at or below each row, 64 at a time.
-// Measured (MI355X): 400 thousand rows of 16 requests out of 8-bit pages 139 us,
-// 5.2 TB/s read and written (a copy of 2 GiB: 4.9); 1000 bf16 slots 3.2 us.
+// Measured (MI355X): 400 thousand rows of 16 requests out of 8-bit pages 134-139 us,
+// 5.2-5.4 TB/s read and written (a copy of 2 GiB: 4.9); 1000 bf16 slots 3.2 us.
 constexpr int kLoadThreads = 256;
 constexpr int kLoadRows = 8;
 

@@ -24,10 +24,10 @@
 //
 // Measured (MI355X): a prompt of 8192 tokens x 32 heads 684-760 us over several
 // cards, 900-1005 TFLOP/s, where a large library matrix product reaches 1255-1365:
-// the matrix cores are busy 50 % of the time, and the softmax's vector
-// instructions (157 to 40 matrix ones a tile, 32 of them exponentials) take the
-// other half; LDS 27 %.  Six chunks of 1 to 1500 tokens behind 0 to 5000 cached
-// ones x 20 heads 223-245 us, up to 745 TFLOP/s: bound by the longest units, 6500
+// the matrix cores are busy 49 % of the time, and the softmax's vector
+// instructions (160 to 40 matrix ones a tile, 32 of them exponentials) take the
+// other half; LDS 26 %.  Six chunks of 1 to 1500 tokens behind 0 to 5000 cached
+// ones x 20 heads 223-268 us, up to 745 TFLOP/s: bound by the longest units, 6500
 // keys at 2.4 us a tile with two workgroups on a CU.  (The output written from the
 // accumulators, 8 bytes a lane, and lane offsets that did not fit the registers
 // cost 743 us instead of 716; head after head instead of block after block 738
@@ -403,7 +403,7 @@ __device__ __forceinline__ void attend_tile(RowState& st, const Stage& t, const 
       scale_log2 = 1.0f;
     }
   }
-  // Weights in bf16 (the matrix cores' type): an unbiased half step of 2^-9 on
+  // Weights in bf16 (the matrix cores' type): an unbiased rounding of at most 2^-8 on
   // each, as large as the rounding of the result itself.  The sum keeps them in
   // fp32, a tile at a time: added to the running sum one by one, a long row's many
   // small weights would each be rounded against it (131072 equal ones 3e-4 off).

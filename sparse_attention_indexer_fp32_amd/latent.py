@@ -4,7 +4,9 @@ Argument marshalling only, as in the package's other calls: every step runs in
 the library's HIP kernels, on `stream` (default: torch's current stream of the
 tensors' device), and a call that cannot be made raises.  Outputs and
 workspaces that the caller does not pass come from torch's allocator on that
-stream, so captured graphs and concurrent streams share none.
+stream, so captured graphs and concurrent streams share none.  With `stream`, the caller
+keeps the inputs (and orders their producers) until the call is done there,
+as for any work on another stream than a tensor's own.
 """
 from __future__ import annotations
 
@@ -233,7 +235,7 @@ def latent_cache_store(kv, slot_map, latent, rope, scale=None, norm_weight=None,
     rotation of the rotary key (with positions and cos_sin), 8-bit codes and a
     scale per token (with scale), in one pass.
 
-    kv (T, 512 + 64) bfloat16 with any row stride; slot_map (T,) int32: tokens
+    kv (T, 512 + 64) bfloat16, rows that do not overlap; slot_map (T,) int32: tokens
     with a slot outside the cache are skipped, and no two may name one slot;
     latent (slots, 512) bfloat16, or uint8 codes with scale (slots,) float32;
     rope (slots, 64) bfloat16; norm_weight (512,) bfloat16; positions (T,)
@@ -330,11 +332,11 @@ def latent_attention(q, latent, rope, indices, softmax_scale: float, scale=None,
                      stream=None) -> Tuple[object, object]:
     """Latent attention, absorbed form, over selected slots.
 
-    q (T, H, 512 + 64) bfloat16 with any token and head strides; indices (T, k)
+    q (T, H, 512 + 64) bfloat16 with any token stride, heads that do not overlap; indices (T, k)
     int32 slots in any order (topk_transform's out; -1 selects nothing);
     latent, rope, scale: the cache.  Returns out (T, H, 512) bfloat16 and lse
     (T, H) float32, the natural logarithm of the softmax's sum.  A token that
-    selects nothing gets zeros and -inf.
+    selects nothing gets zeros and -inf, a head with a score of NaN or +inf NaN in both.
     """
     dev, at = _gpu(q, "q")
     T, H, qargs = _queries(q, _QUERY)
