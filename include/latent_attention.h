@@ -170,9 +170,9 @@ topk_status_t latent_cache_load_paged(const int32_t* page_table, const int32_t* 
  * weighs nothing.
  * Scores, statistics and sums are fp32; the weights are rounded to bf16 for
  * the matrix cores, and the result once at the end.
- * Any score that is finite in fp32 counts as what it is.  Weights are relative to a
- * reference up to 2^8 below the largest and are divided by their sum at the end,
- * so values beyond 2^120 / keys in magnitude may overflow.
+ * Any score that is finite in fp32 counts as what it is.  Weights are as large as
+ * 2^8 until they are divided by their sum at the end, so values beyond 2^120 / keys
+ * in magnitude may overflow.
  *
  *   workspace, workspace_bytes: device memory for partial results, at least
  *            what latent_attention_workspace says for (num_tokens, num_heads,

@@ -88,9 +88,9 @@ topk_status_t check_cache(const void* latent, int64_t latent_stride, const uint1
 constexpr int64_t kMaxTileStride = (1 << 24) - 8;
 
 // The kernels' scale: in log2 units, and not quite 0, which would make 0 * -inf
-// of a masked score (2^-100 leaves every score as good as 0).
+// of a masked score (2^-149, the least there is, leaves every finite score below 2^-21).
 float scale_log2(float softmax_scale) {
-  return softmax_scale == 0.f ? 0x1p-100f : softmax_scale * 1.44269504088896340736f;
+  return softmax_scale == 0.f ? 0x1p-149f : softmax_scale * 1.44269504088896340736f;
 }
 
 // Tiles of a token that attends `keys` keys, and one more: an upper bound for what the kernel counts.

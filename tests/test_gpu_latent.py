@@ -965,3 +965,36 @@ def test_store_more_tokens_than_a_launch_has_threads_for(lib, dev):
     assert torch.equal(whole[0], few[0]) and torch.equal(whole[1], few[1]) and bool(few[0][:-1].any(1).all())
     del kv, slot_map, positions
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("shape", sorted(SHAPES))
+def test_scale_of_zero(lib, dev, shape):
+    """With scale 0 every key weighs the same, however large its product, and
+    masked ones still nothing."""
+    import torch
+    T, H, k = SHAPES[shape]
+    rng = np.random.default_rng(38)
+    cache = Cache(rng, 3000, False, dev)
+    q, _ = _bf(rng, (T, H, 576), dev)
+    q[:, :, 512 + 5] = 2.0 ** 110
+    idx = np.stack([rng.permutation(3000)[:k] for _ in range(T)])
+    idx[:, ::7] = -1
+    n = int((idx[0] >= 0).sum())
+    for form, out, lse in _both_absorbed(lib, dev, cache, q, idx, 0.0):
+        out, lse = _host(out), _host(lse)
+        assert (np.abs(lse - np.log(n)) <= 2.0 ** -20 + (2 * k + 8) * lo.U32).all(), form
+        for t in range(min(T, 6)):
+            rows = cache.c[idx[t][idx[t] >= 0]]
+            bound = lo.U16 * np.abs(rows.mean(0)) + (4 * k * lo.U32 + 2.0 ** -18) * np.abs(rows).mean(0)
+            for h in (0, H - 1):
+                assert lo.check(f"{form} token {t}", out[t, h], rows.mean(0), bound) is None
+    kv, kvh = _bf(rng, (k, 2, 256), dev)
+    rope = _bf(rng, (k, 64), dev)[0]
+    qe = q[:3, :2, :192].contiguous()
+    qe[:, :, 128 + 5] = 2.0 ** 110
+    out, lse = lib.latent_attention_expanded(qe, kv, rope, _i32([0, 3], dev), _i32([0, k], dev), 0.0)
+    for i in range(3):
+        v = kvh[:k - 2 + i, :, 128:]
+        assert (np.abs(_host(lse)[i] - np.log(len(v))) <= 2.0 ** -20 + (2 * k + 8) * lo.U32).all()
+        bound = lo.U16 * np.abs(v.mean(0)) + (4 * k * lo.U32 + 2.0 ** -18) * np.abs(v).mean(0)
+        assert lo.check(f"query {i}", _host(out)[i], v.mean(0), bound) is None
