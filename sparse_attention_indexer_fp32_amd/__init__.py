@@ -5,8 +5,8 @@ HIP kernels.  PyTorch supplies device memory and the current stream.  There is
 no fallback: if the library is not built, or the call fails, this raises.
 
 The C entry points have the same names; see include/topk_transform.h,
-include/indexer_topk.h and include/latent_attention.h for the argument meaning,
-layouts, ownership and error behaviour.
+include/indexer_topk.h, include/indexer_paged.h and include/latent_attention.h for
+the argument meaning, layouts, ownership and error behaviour.
 """
 from __future__ import annotations
 
@@ -15,10 +15,13 @@ import os
 from typing import Optional, Tuple
 
 from . import latent as _latent
+from . import paged_indexer as _paged_indexer
 from .build import LIB_PATH
 from .latent import (EXPORTED_LATENT, LATENT_DIM, LATENT_HEAD_DIM, LATENT_ROPE_DIM, AppendPlan, latent_attention,
                      latent_attention_expanded, latent_attention_paged, latent_cache_load, latent_cache_load_paged,
                      latent_cache_store, paged_append_plan)
+from .paged_indexer import (EXPORTED_INDEXER_PAGED, INDEXER_ROPE_DIM, indexer_cache_load_paged, indexer_cache_store,
+                            indexer_logits_paged, indexer_queries)
 
 TOPK_MAX_K = 2048
 STREAM_SHAPES = 3   # compiled streaming-kernel shapes: topk_set_stream_shape accepts -1 and 0..STREAM_SHAPES-1
@@ -96,6 +99,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.indexer_set_select_mode.argtypes = [c_i32]
     lib.indexer_set_select_mode.restype = ctypes.c_int
     _latent.declare(lib)
+    _paged_indexer.declare(lib)
     _lib = lib
     return lib
 
