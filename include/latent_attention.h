@@ -211,6 +211,38 @@ topk_status_t latent_attention_paged(const uint16_t* q, int64_t q_token_stride, 
 topk_status_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, int64_t keys, size_t* bytes);
 
 /*
+ * latent_attention_shared -- absorbed form over whole cached sequences that share
+ * prefixes, each read once for all of the tokens behind it.
+ *
+ *   group_starts (num_groups + 1,) int32, ascending: requests [group_starts[g],
+ *            group_starts[g + 1]) are group g; requests of no group share nothing.
+ *   shared_lens (num_groups,) int32: the first shared_lens[g] positions of a
+ *            group's requests hold the same tokens.  They are read through the page table row of the
+ *            group's first request; the other requests' pages of them are not looked at.
+ * The i-th of request b's n new tokens attends its group's positions [0,
+ * shared_lens[g]) and its own [shared_lens[g], seq_lens[b] - n + i + 1).  Prefixes are
+ * meant to end before the new tokens; where one does not, it counts whole for
+ * every token of the group.  Lengths beyond pages_per_row * page_size are cut to that.
+ * Other arguments, padding and missing pages as latent_attention_paged; the
+ * workspace is latent_attention_shared_workspace's.  Many tokens are taken some thousands at
+ * a time, each with its own read of the prefixes.  One row of (token, head) pairs of a call, its heads
+ * times its positions / 2048, must stay below 2^30, and num_heads at most 2^24.
+ */
+topk_status_t latent_attention_shared(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                      const void* latent, int64_t latent_stride, const uint16_t* rope,
+                                      int64_t rope_stride, const float* scale, int32_t cache_type,
+                                      const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_starts,
+                                      const int32_t* group_starts, const int32_t* shared_lens, int32_t page_size,
+                                      float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream, int32_t num_tokens,
+                                      int32_t num_heads, int32_t num_requests, int32_t num_groups,
+                                      int64_t pages_per_row, int64_t num_slots);
+
+/* Bytes of workspace for up to num_tokens tokens of num_heads heads (on the current
+ * device); it grows with the tokens, to about 1 GB. */
+topk_status_t latent_attention_shared_workspace(int32_t num_tokens, int32_t num_heads, size_t* bytes);
+
+/*
  * latent_attention_expanded -- expanded form over ragged batches (prompts,
  * with or without a cached prefix).
  *

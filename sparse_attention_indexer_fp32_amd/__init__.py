@@ -18,8 +18,8 @@ from . import latent as _latent
 from . import paged_indexer as _paged_indexer
 from .build import LIB_PATH
 from .latent import (EXPORTED_LATENT, LATENT_DIM, LATENT_HEAD_DIM, LATENT_ROPE_DIM, AppendPlan, latent_attention,
-                     latent_attention_expanded, latent_attention_paged, latent_cache_load, latent_cache_load_paged,
-                     latent_cache_store, paged_append_plan)
+                     latent_attention_expanded, latent_attention_paged, latent_attention_shared, latent_cache_load,
+                     latent_cache_load_paged, latent_cache_store, paged_append_plan)
 from .paged_indexer import (EXPORTED_INDEXER_PAGED, INDEXER_ROPE_DIM, indexer_cache_load_paged, indexer_cache_store,
                             indexer_logits_paged, indexer_queries)
 

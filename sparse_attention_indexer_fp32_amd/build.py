@@ -15,8 +15,8 @@ LIB_NAME = "libtopk_transform.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["topk_kernels.hip", "topk_api.cpp", "indexer_kernels.hip", "indexer_api.cpp", "cache_kernels.hip",
-           "attend_kernels.hip", "prefill_kernels.hip", "latent_api.cpp", "indexer_cache_kernels.hip",
-           "indexer_paged_kernels.hip", "indexer_paged_api.cpp"]
+           "attend_kernels.hip", "shared_kernels.hip", "prefill_kernels.hip", "latent_api.cpp",
+           "indexer_cache_kernels.hip", "indexer_paged_kernels.hip", "indexer_paged_api.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -402,6 +402,86 @@ topk_status_t latent_attention_paged(const uint16_t* q, int64_t q_token_stride, 
                 stream);
 }
 
+topk_status_t latent_attention_shared_workspace(int32_t num_tokens, int32_t num_heads, size_t* bytes) {
+  topk::set_last_error("");
+  if (!bytes) return invalid("bytes must be non-null");
+  if (num_tokens < 0 || num_heads < 0) return invalid("num_tokens and num_heads must be >= 0");
+  *bytes = 0;
+  if (num_tokens == 0 || num_heads == 0) return TOPK_SUCCESS;
+  int cus = 0;
+  const topk_status_t st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  *bytes = latent::shared_layout(latent::shared_tokens(num_tokens, num_heads, 0), num_heads, cus).total();
+  return TOPK_SUCCESS;
+}
+
+topk_status_t latent_attention_shared(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                      const void* latent, int64_t latent_stride, const uint16_t* rope,
+                                      int64_t rope_stride, const float* scale, int32_t cache_type,
+                                      const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_starts,
+                                      const int32_t* group_starts, const int32_t* shared_lens, int32_t page_size,
+                                      float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream, int32_t num_tokens,
+                                      int32_t num_heads, int32_t num_requests, int32_t num_groups,
+                                      int64_t pages_per_row, int64_t num_slots) {
+  topk::set_last_error("");
+  latent::SharedArgs a{};
+  topk_status_t st = check_cache(latent, latent_stride, rope, rope_stride, scale, cache_type, num_slots, &a.cache);
+  if (st != TOPK_SUCCESS) return st;
+  st = check_queries(q, q_token_stride, q_head_stride, out, num_tokens, num_heads, LATENT_DIM + LATENT_ROPE_DIM);
+  if (st != TOPK_SUCCESS) return st;
+  a.log2_page = log2_of(page_size);
+  if (a.log2_page < 0) return invalid("page_size must be a power of two");
+  if (num_requests < 0 || num_groups < 0 || pages_per_row < 0 || pages_per_row > (int64_t)INT32_MAX)
+    return invalid("num_requests and num_groups must be >= 0 and pages_per_row in [0, 2^31)");
+  if ((int64_t)num_requests + num_groups > (int64_t)INT32_MAX) return invalid("num_requests and num_groups must be below 2^31 together");
+  if (num_heads > 1 << 24) return invalid("num_heads must be at most 2^24");
+  if (num_tokens == 0 || num_heads == 0 || num_requests == 0) return TOPK_SUCCESS;
+  if (!seq_lens || !q_starts || (pages_per_row > 0 && !page_table))
+    return invalid("page_table, seq_lens and q_starts must be non-null");
+  if (num_groups > 0 && (!group_starts || !shared_lens)) return invalid("group_starts and shared_lens must be non-null");
+  const int64_t keys = pages_per_row * (int64_t)page_size;
+  const int at_once = latent::shared_tokens(num_tokens, num_heads, keys);
+  if (at_once == 0) return invalid("more heads and positions than the tiles of a launch are counted in");
+  int cus = 0;
+  st = device_cus(&cus);
+  if (st != TOPK_SUCCESS) return st;
+  const latent::SplitLayout s = latent::shared_layout(at_once, num_heads, cus);
+  if (!workspace || workspace_bytes < s.total()) return invalid("the workspace is smaller than latent_attention_shared_workspace says");
+  if (!aligned(workspace)) return invalid("the workspace must start on a 16-byte boundary");
+  char* p = static_cast<char*>(workspace);
+  a.part_out = reinterpret_cast<float*>(p);
+  a.part_ml = reinterpret_cast<float2*>(p + s.out_bytes);
+  a.part_rec = reinterpret_cast<int4*>(p + s.out_bytes + s.ml_bytes);
+  a.q = q;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.q_starts = q_starts;
+  a.group_starts = group_starts;
+  a.shared_lens = shared_lens;
+  a.pages_per_row = pages_per_row;
+  a.num_requests = num_requests;
+  a.num_groups = num_groups;
+  a.scale_log2 = scale_log2(softmax_scale);
+  a.out = out;
+  a.lse = lse;
+  a.num_heads = num_heads;
+  a.wgs = cus;
+  for (int64_t t = 0; t < num_tokens; t += at_once) {
+    a.first_token = (int32_t)t;
+    a.num_tokens = (int32_t)(num_tokens - t < at_once ? num_tokens - t : at_once);
+    a.pieces = latent::shared_pieces(a.num_tokens, num_heads);
+    const hipError_t e = latent::launch_shared(a, cache_type == LATENT_CACHE_E4M3, stream);
+    if (e != hipSuccess) return launched(e, "latent-attention shared");
+  }
+  char buf[96];
+  std::snprintf(buf, sizeof(buf), "latent-attention shared %s tokens=%d wgs=%d", cache_type == LATENT_CACHE_E4M3 ? "e4m3" : "bf16",
+                at_once, a.wgs);
+  return launched(hipSuccess, buf);
+}
+
 topk_status_t latent_attention_expanded_workspace(int32_t num_tokens, int32_t num_heads, int64_t num_kv,
                                                   int32_t num_requests, size_t* bytes) {
   topk::set_last_error("");

@@ -127,7 +127,45 @@ SplitLayout split_layout(int num_tokens, int num_heads, int wgs);
 int64_t attend_threads(int num_tokens, int num_heads);     // the most of any launch of the call
 hipError_t launch_attend(const AttendArgs& a, bool e4m3, hipStream_t stream);
 
-// Expanded form.
+// Absorbed form over whole sequences that share prefixes.  A unit is 64
+// neighbouring rows of (token, head) pairs of one group against its shared
+// prefix, or of one request against its own keys.  `wgs` workgroups share all
+// units' tiles evenly; every unit's parts go to the workspace and are joined by a
+// second launch.  Tokens are taken `shared_tokens` at a time.
+constexpr int kUnitWaves = 4;
+constexpr int kUnitRows = 16 * kUnitWaves;
+constexpr int kSharedTiles = 4;      // tiles a workgroup takes at least
+struct SharedArgs {
+  const uint16_t* q;
+  int64_t q_token_stride, q_head_stride;   // elements
+  Cache cache;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* q_starts;
+  const int32_t* group_starts;
+  const int32_t* shared_lens;
+  int64_t pages_per_row;
+  int32_t num_requests;
+  int32_t num_groups;
+  int32_t log2_page;
+  float scale_log2;          // softmax scale * log2(e)
+  uint16_t* out;
+  float* lse;                // or nullptr
+  int32_t first_token;       // of this launch
+  int32_t num_tokens;        // of this launch
+  int32_t num_heads;
+  int32_t wgs;
+  int32_t pieces;            // of 16 rows, that units of one kind may have
+  // workspace (shared_layout)
+  float* part_out;
+  float2* part_ml;
+  int4* part_rec;            // two a row: its places in the parts of the group's unit, and of the request's
+};
+int shared_tokens(int num_tokens, int num_heads, int64_t keys);
+int shared_pieces(int num_tokens, int num_heads);
+SplitLayout shared_layout(int num_tokens, int num_heads, int wgs);
+hipError_t launch_shared(const SharedArgs& a, bool e4m3, hipStream_t stream);
+
 // Expanded form.  A unit is a block of 128 queries of one head.  Split: `wgs`
 // workgroups share all units' tiles of 64 keys evenly, as above.
 constexpr int kPlanRequests = 512;       // requests a split launch takes at most

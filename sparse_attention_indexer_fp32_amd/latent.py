@@ -23,6 +23,7 @@ _BF16, _E4M3 = 0, 1
 
 EXPORTED_LATENT = ("paged_append_plan", "latent_cache_store", "latent_cache_load", "latent_cache_load_paged",
                    "latent_attention", "latent_attention_paged", "latent_attention_workspace",
+                   "latent_attention_shared", "latent_attention_shared_workspace",
                    "latent_attention_expanded", "latent_attention_expanded_workspace")
 
 
@@ -48,6 +49,9 @@ def declare(lib: ctypes.CDLL) -> None:
         "latent_attention_paged": [vp, i64, i64] + cache + [vp, vp, vp, i32, f32, vp, vp, vp, size, vp, i32, i32, i32,
                                                             i64, i64],
         "latent_attention_workspace": [i32, i32, i64, ctypes.POINTER(size)],
+        "latent_attention_shared": [vp, i64, i64] + cache + [vp, vp, vp, vp, vp, i32, f32, vp, vp, vp, size, vp, i32, i32,
+                                                             i32, i32, i64, i64],
+        "latent_attention_shared_workspace": [i32, i32, ctypes.POINTER(size)],
         "latent_attention_expanded": [vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, f32, i32, vp, vp, vp, size, vp, i32,
                                       i64, i32, i32],
         "latent_attention_expanded_workspace": [i32, i32, i64, i32, ctypes.POINTER(size)],
@@ -387,6 +391,46 @@ def latent_attention_paged(q, latent, rope, page_table, seq_lens, q_starts, page
                 float(softmax_scale), got[0].data_ptr(), got[1].data_ptr(), got[3], got[4], handle, T, H, B, P, slots)
 
     _call("latent_attention_paged", dev, stream, args)
+    return got[0], got[1]
+
+
+def latent_attention_shared(q, latent, rope, page_table, seq_lens, q_starts, group_starts, shared_lens, page_size: int,
+                            softmax_scale: float, scale=None, out=None, lse=None, stream=None) -> Tuple[object, object]:
+    """Latent attention, absorbed form, over whole cached sequences that share
+    prefixes, each read once for all of the tokens behind it.
+
+    Requests [group_starts[g], group_starts[g + 1]) are group g (group_starts (G + 1,) int32, ascending),
+    and their first shared_lens[g] positions (shared_lens (G,) int32) hold the
+    same tokens, found through the page table row of the group's first request.
+    The i-th of request b's n tokens attends these and its own positions
+    [shared_lens[g], seq_lens[b] - n + i + 1).  Requests of no group share
+    nothing.  Other arguments and the return value as in latent_attention_paged.
+    """
+    dev, at = _gpu(q, "q")
+    T, H, qargs = _queries(q, _QUERY)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be (requests, pages)")
+    B, P = page_table.shape
+    _int32("page_table", page_table, (B, P), at)
+    _int32("seq_lens", seq_lens, (B,), at)
+    _int32("q_starts", q_starts, (B + 1,), at)
+    if shared_lens.dim() != 1:
+        raise ValueError("shared_lens must be (groups,)")
+    G = shared_lens.shape[0]
+    _int32("shared_lens", shared_lens, (G,), at)
+    _int32("group_starts", group_starts, (G + 1,), at)
+    cache, slots = _cache(latent, rope, scale, at)
+    _outputs(out, lse, T, H, LATENT_DIM, at)
+    got = []
+
+    def args(handle):
+        got.extend(_made(out, lse, T, H, LATENT_DIM, dev))
+        got.extend(_workspace(dev, "latent_attention_shared_workspace", T, H))
+        return (*qargs, *cache, page_table.data_ptr(), seq_lens.data_ptr(), q_starts.data_ptr(), group_starts.data_ptr(),
+                shared_lens.data_ptr(), int(page_size), float(softmax_scale), got[0].data_ptr(), got[1].data_ptr(), got[3],
+                got[4], handle, T, H, B, G, P, slots)
+
+    _call("latent_attention_shared", dev, stream, args)
     return got[0], got[1]
 
 
