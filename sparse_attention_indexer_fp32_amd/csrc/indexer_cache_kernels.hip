@@ -14,16 +14,25 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kHeads = 32;
 constexpr int kDim = 128;
 constexpr int kRope = 64;
-constexpr int kLanes = 16;                // lanes of a row, 8 values each
+constexpr int kLanes = 4;                 // lanes of a row
+constexpr int kChunks = 4;                // chunks of 8 values that a lane holds of it
 constexpr int kThreads = 256;
 constexpr int kRowsPerWg = kThreads / kLanes;
 constexpr int64_t kMaxWgs = UINT32_MAX / kThreads;   // along x: the hardware counts threads in 32 bits
 
-// ---- a row over 16 lanes ----------------------------------------------------------------------
+// ---- a row over four lanes --------------------------------------------------------------------
 
-// A row of 128 values lies in the 16 lanes of a DPP row, lane l holding values
-// 8 l .. 8 l + 7 (one 16-byte load): sums, maxima and the mixing's exchanges between
-// lanes are DPP moves, and nothing passes through LDS.
+// A row of 128 values lies in the four lanes of a quad: lane l holds the chunks of 8
+// values l, 4 + l, 8 + l and 12 + l (16-byte loads, 64 bytes of a row to an instruction), so value 8
+// c + e sits in lane c % 4.  Of the mixing's seven rounds five and both kinds of
+// rotation (neighbours, and values 32 apart) then stay within the lane, all lanes
+// turn as many values as the others, and what is left are exchanges within a quad, DPP moves.
+// (16 lanes of 8 values each, where four rounds cross lanes and half of the lanes
+// have nothing to turn: 8192 tokens x 32 heads 53 us against TIME.)
+struct Row {
+  float v[kChunks * 8];      // chunk after chunk
+};
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, true);
@@ -32,31 +41,18 @@ template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
 }
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kXor7 = 0x141, kXor15 = 0x140;   // quad_perm (3 of them), row_half_mirror, row_mirror
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E;      // quad_perm
 
-__device__ __forceinline__ float from_xor4(float v) { return dpp<kXor3>(dpp<kXor7>(v)); }
-__device__ __forceinline__ float from_xor8(float v) { return dpp<kXor7>(dpp<kXor15>(v)); }
-
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float quad_sum(float v) {
   v += dpp<kXor1>(v);
   v += dpp<kXor2>(v);
-  v += dpp<kXor7>(v);
-  v += dpp<kXor15>(v);
   return v;
 }
 
 __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  v = max_u32(v, dpp<kXor1>(v));
-  v = max_u32(v, dpp<kXor2>(v));
-  v = max_u32(v, dpp<kXor7>(v));
-  v = max_u32(v, dpp<kXor15>(v));
-  return v;
-}
-
 // Eight values of a vector of either type.
-__device__ __forceinline__ void load8(const void* from, int fp32, int at, float (&v)[8]) {
+__device__ __forceinline__ void load8(const void* from, int fp32, int at, float* v) {
   if (fp32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(from) + at);
     const float4 a = p[0], b = p[1];
@@ -69,107 +65,101 @@ __device__ __forceinline__ void load8(const void* from, int fp32, int at, float 
   }
 }
 
-// The angles of a lane's values: interleaved, 4 pairs lie in the lane; by
-// halves, value 8 l + j turns with that of lane l ^ 4 by angle (8 l + j) % 32.
+__device__ __forceinline__ void load_row(const uint16_t* from, int l, Row& r) {
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) load8(from, 0, 32 * c + 8 * l, r.v + 8 * c);
+}
+
+// The angles of a lane's values.  Interleaved: those of the four pairs of
+// chunk l, then of chunk 4 + l.  By halves chunk l turns with chunk 4 + l, by its 8 angles.
 struct Angles {
   float c[8], s[8];
 };
 __device__ __forceinline__ void load_angles(const TurnArgs& t, int64_t pos, int l, Angles& a) {
-  if (l >= kRope / 8) return;
   const float* row = t.cos_sin + pos * kRope;
-  if (t.interleaved) {
-    const float4 c = *reinterpret_cast<const float4*>(row + 4 * l);
-    const float4 s = *reinterpret_cast<const float4*>(row + kRope / 2 + 4 * l);
-    a.c[0] = c.x; a.c[1] = c.y; a.c[2] = c.z; a.c[3] = c.w;
-    a.s[0] = s.x; a.s[1] = s.y; a.s[2] = s.z; a.s[3] = s.w;
-  } else {
-    load8(row, 1, 8 * (l & 3), a.c);
-    load8(row + kRope / 2, 1, 8 * (l & 3), a.s);
+  const int second = t.interleaved ? 16 + 4 * l : 8 * l + 4, first = t.interleaved ? 4 * l : 8 * l;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const float4 c = *reinterpret_cast<const float4*>(row + (half ? second : first));
+    const float4 s = *reinterpret_cast<const float4*>(row + kRope / 2 + (half ? second : first));
+    a.c[4 * half] = c.x; a.c[4 * half + 1] = c.y; a.c[4 * half + 2] = c.z; a.c[4 * half + 3] = c.w;
+    a.s[4 * half] = s.x; a.s[4 * half + 1] = s.y; a.s[4 * half + 2] = s.z; a.s[4 * half + 3] = s.w;
   }
 }
 
-__device__ __forceinline__ void rotate(int interleaved, int l, const Angles& a, float (&y)[8]) {
+__device__ __forceinline__ void turn(float& u, float& v, float c, float s) {
+  const float a = u * c - v * s;
+  v = v * c + u * s;
+  u = a;
+}
+
+__device__ __forceinline__ void rotate(int interleaved, const Angles& a, Row& r) {
   if (interleaved) {
-    if (l < kRope / 8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = y[2 * i], v = y[2 * i + 1];
-        y[2 * i] = u * a.c[i] - v * a.s[i];
-        y[2 * i + 1] = v * a.c[i] + u * a.s[i];
-      }
-    }
+    for (int i = 0; i < 8; ++i) turn(r.v[2 * i], r.v[2 * i + 1], a.c[i], a.s[i]);
   } else {
-    float o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = from_xor4(y[i]);     // every lane takes part
-    if (l < kRope / 8) {
-      const float sign = l < kRope / 16 ? -1.0f : 1.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * a.c[i] + sign * o[i] * a.s[i];
-    }
+    for (int i = 0; i < 8; ++i) turn(r.v[i], r.v[8 + i], a.c[i], a.s[i]);
   }
 }
 
-// y[i] = sum_j (-1)^popcount(i & j) x[j] / sqrt(128): seven rounds of sums and
-// differences, three within the lane and four between lanes, 56 additions a lane
-// where the matrix takes 1024 products.
-__device__ __forceinline__ void mix(int l, float (&y)[8]) {
+// y[i] = sum_j (-1)^popcount(i & j) x[j]: seven rounds of sums and differences, 288
+// instructions a lane where the matrix takes 4096 products.  (The factor 1 / sqrt(128) is left to the scale.)
+__device__ __forceinline__ void mix(int l, Row& r) {
+  float (&v)[8 * kChunks] = r.v;
 #pragma unroll
-  for (int bit = 1; bit < 8; bit <<= 1)
+  for (int bit = 1; bit < 8 * kChunks; bit <<= 1)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8 * kChunks; ++i)
       if (!(i & bit)) {
-        const float u = y[i], v = y[i | bit];
-        y[i] = u + v;
-        y[i | bit] = u - v;
+        const float a = v[i], b = v[i | bit];
+        v[i] = a + b;
+        v[i | bit] = a - b;
       }
-  const float s1 = l & 1 ? -1.0f : 1.0f, s2 = l & 2 ? -1.0f : 1.0f, s4 = l & 4 ? -1.0f : 1.0f, s8 = l & 8 ? -1.0f : 1.0f;
+  const float s1 = l & 1 ? -1.0f : 1.0f, s2 = l & 2 ? -1.0f : 1.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v = y[i];
-    v = fmaf(v, s1, dpp<kXor1>(v));
-    v = fmaf(v, s2, dpp<kXor2>(v));
-    v = fmaf(v, s4, from_xor4(v));
-    v = fmaf(v, s8, from_xor8(v));
-    y[i] = v * 0.08838834764831845f;
+  for (int i = 0; i < 8 * kChunks; ++i) {
+    v[i] = fmaf(v[i], s1, dpp<kXor1>(v[i]));
+    v[i] = fmaf(v[i], s2, dpp<kXor2>(v[i]));
   }
 }
 
-// The row's scale and this lane's eight codes.  The largest magnitude is an
-// integer maximum of the bits without the sign: infinities and NaN come out on top,
-// and such a row's scale is NaN.  A subnormal scale would have no finite inverse: rows
-// below 448 * 2^-126 take the smallest normal one.
-__device__ __forceinline__ float quantise(const float (&y)[8], uint2& codes) {
+// The scale of a row that is still to be multiplied by `factor`, and this lane's codes.  The largest
+// magnitude is an integer maximum of the bits without the sign: infinities and
+// NaN come out on top, and such a row's scale is NaN.  The codes are the row times the
+// reciprocal of its step, which moves what lies within two units of fp32 from a tie.  A step that is
+// subnormal would have no finite reciprocal: rows below 448 * 2^-126 take the smallest normal one.
+__device__ __forceinline__ float quantise(const Row& r, float factor, uint2 (&codes)[kChunks]) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_u32(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-  const float amax = __uint_as_float(row_max(top));
-  const float scale = amax == 0.f                             ? 1.0f
-                      : !(amax < INFINITY)                     ? __uint_as_float(0x7FC00000u)
-                      : amax < 448.0f * 1.17549435e-38f ? 1.17549435e-38f
-                                                               : amax / 448.0f;
-  // The quotient by the reciprocal, corrected by its remainder (Markstein's
-  // step), is rounded as a division's, unless the remainder leaves the normal numbers.
-  float v[8];
-  if (scale > 0x1p-60f) {
-    const float inv = 1.0f / scale;
+  for (int i = 0; i < 8 * kChunks; ++i) top = max_u32(top, __float_as_uint(r.v[i]) & 0x7FFFFFFFu);
+  top = max_u32(top, dpp<kXor1>(top));
+  top = max_u32(top, dpp<kXor2>(top));
+  const float amax = __uint_as_float(top);
+  const float step = amax == 0.f                             ? 1.0f
+                     : !(amax < INFINITY)                     ? __uint_as_float(0x7FC00000u)
+                     : amax < 448.0f * 1.17549435e-38f ? 1.17549435e-38f
+                                                              : amax / 448.0f;
+  const float inv = 1.0f / step;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = y[i] * inv;
-      v[i] = fmaf(fmaf(-q, scale, y[i]), inv, q);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = y[i] / scale;
+  for (int c = 0; c < kChunks; ++c) {
+    const float* v = r.v + 8 * c;
+    int lo = 0, hi = 0;
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, hi, true);
+    codes[c] = make_uint2((uint32_t)lo, (uint32_t)hi);
   }
-  int lo = 0, hi = 0;
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
-  codes = make_uint2((uint32_t)lo, (uint32_t)hi);
-  return scale;
+  return amax == 0.f ? 1.0f : step * factor;
 }
+
+__device__ __forceinline__ void store_codes(uint8_t* to, int l, const uint2 (&codes)[kChunks]) {
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) *reinterpret_cast<uint2*>(to + 32 * c + 8 * l) = codes[c];
+}
+
+constexpr float kMixFactor = 0.08838834764831845f;   // 1 / sqrt(128)
 
 __device__ __forceinline__ int64_t workgroup() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
@@ -178,14 +168,18 @@ __device__ __forceinline__ int64_t workgroup() { return (int64_t)blockIdx.y * gr
 __global__ __launch_bounds__(kThreads) void key_store_kernel(StoreArgs a) {
   const int l = threadIdx.x & (kLanes - 1);
   const int64_t t = workgroup() * kRowsPerWg + threadIdx.x / kLanes;
-  // lanes of a row leave together, so the others' DPP moves stay within whole rows
+  // (lanes of a row leave together, so the others' DPP moves stay within whole rows)
   if (t >= a.num_tokens) return;
+  // all that depends on nothing is loaded first; only the angles wait for a load
   const int64_t slot = a.slot_map[t], pos = a.turn.cos_sin ? a.turn.positions[t] : 0;
-  float y[8], w[8], bias[8];
-  load8(a.k + t * a.k_stride, 0, 8 * l, y);
+  Row y, w, bias;
+  load_row(a.k + t * a.k_stride, l, y);
   if (a.norm_weight) {
-    load8(a.norm_weight, a.norm_fp32, 8 * l, w);
-    load8(a.norm_bias, a.norm_fp32, 8 * l, bias);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      load8(a.norm_weight, a.norm_fp32, 32 * c + 8 * l, w.v + 8 * c);
+      load8(a.norm_bias, a.norm_fp32, 32 * c + 8 * l, bias.v + 8 * c);
+    }
   }
   if (slot < 0 || slot >= a.num_slots) return;
   Angles angles;
@@ -197,23 +191,23 @@ __global__ __launch_bounds__(kThreads) void key_store_kernel(StoreArgs a) {
     // two passes over the registers: the variance of values far from 0 keeps its digits
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += y[i];
-    const float mean = row_sum(sum) * (1.0f / kDim);
+    for (int i = 0; i < 8 * kChunks; ++i) sum += y.v[i];
+    const float mean = quad_sum(sum) * (1.0f / kDim);
     float sq = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[i] -= mean;
-      sq = fmaf(y[i], y[i], sq);
+    for (int i = 0; i < 8 * kChunks; ++i) {
+      y.v[i] -= mean;
+      sq = fmaf(y.v[i], y.v[i], sq);
     }
-    const float inv = 1.0f / sqrtf(row_sum(sq) * (1.0f / kDim) + a.eps);
+    const float inv = 1.0f / sqrtf(quad_sum(sq) * (1.0f / kDim) + a.eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i] * inv, w[i], bias[i]);
+    for (int i = 0; i < 8 * kChunks; ++i) y.v[i] = fmaf(y.v[i] * inv, w.v[i], bias.v[i]);
   }
-  if (a.turn.cos_sin) rotate(a.turn.interleaved, l, angles, y);
+  if (a.turn.cos_sin) rotate(a.turn.interleaved, angles, y);
   if (a.turn.hadamard) mix(l, y);
-  uint2 codes;
-  const float scale = quantise(y, codes);
-  *reinterpret_cast<uint2*>(a.keys + slot * a.key_stride + 8 * l) = codes;
+  uint2 codes[kChunks];
+  const float scale = quantise(y, a.turn.hadamard ? kMixFactor : 1.0f, codes);
+  store_codes(a.keys + slot * a.key_stride, l, codes);
   if (l == 0) a.key_scale[slot] = scale;
 }
 
@@ -225,20 +219,20 @@ __global__ __launch_bounds__(kThreads) void queries_kernel(QueryArgs a) {
   const int h = (int)(row % kHeads);
   if (t >= a.num_tokens) return;
   const int64_t pos = a.turn.cos_sin ? a.turn.positions[t] : 0;
-  float y[8];
-  load8(a.q + t * a.q_token_stride + h * a.q_head_stride, 0, 8 * l, y);
+  Row y;
+  load_row(a.q + t * a.q_token_stride + h * a.q_head_stride, l, y);
   const float weight = a.weight_fp32 ? static_cast<const float*>(a.weights)[t * a.weight_stride + h]
                                      : (float)static_cast<const __bf16*>(a.weights)[t * a.weight_stride + h];
-  Angles angles;
   if (a.turn.cos_sin) {
     if (pos < 0 || pos >= a.turn.max_positions) return;
+    Angles angles;
     load_angles(a.turn, pos, l, angles);
-    rotate(a.turn.interleaved, l, angles, y);
+    rotate(a.turn.interleaved, angles, y);
   }
   if (a.turn.hadamard) mix(l, y);
-  uint2 codes;
-  const float scale = quantise(y, codes);
-  *reinterpret_cast<uint2*>(a.out_q + row * kDim + 8 * l) = codes;
+  uint2 codes[kChunks];
+  const float scale = quantise(y, a.turn.hadamard ? kMixFactor : 1.0f, codes);
+  store_codes(a.out_q + row * kDim, l, codes);
   if (l == 0) a.out_weights[row] = weight * a.weight_scale * scale;
 }
 

@@ -206,13 +206,13 @@ topk_status_t indexer_logits_paged(const uint8_t* q, const float* weights, const
   topk_status_t st = check_paged(keys, key_stride, key_scale, num_slots, page_table, page_size, num_requests, pages_per_row, &a.cache);
   if (st != TOPK_SUCCESS) return st;
   if (num_tokens < 0) return invalid("num_tokens must be >= 0");
-  if (width < 0 || width > (int64_t)INT32_MAX) return invalid("width must be in [0, 2^31)");
+  if (width < 0 || width >= (int64_t)1 << 30) return invalid("width must be in [0, 2^30)");
   if (num_tokens == 0) return TOPK_SUCCESS;
   if (!q || !weights || !q_starts) return invalid("q, weights and q_starts must be non-null");
   if (num_requests > 0 && !seq_lens) return invalid("seq_lens must be non-null");
   if (!aligned(q) || !aligned(weights)) return invalid("q and weights must start on 16-byte boundaries");
   if (!logits && width > 0) return invalid("logits must be non-null");
-  if ((width / 128 + 1) * num_tokens > (int64_t)INT32_MAX) return invalid("more tokens and positions than the tiles of a launch are counted in");
+  if ((width / 64 + 1) * num_tokens > (int64_t)INT32_MAX) return invalid("more tokens and positions than the tiles of a launch are counted in");
   int cus = 0;
   st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;

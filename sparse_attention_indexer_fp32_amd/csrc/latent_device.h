@@ -111,6 +111,18 @@ __device__ __forceinline__ void queue_to_lds(const char* src, uint32_t lds) {
                :: "v"(src), "s"(lds) : "m0", "memory");
 }
 
+// The same for bytes that are read once, by one workgroup: they are not kept in the caches (64 requests of
+// 34816 index keys, 290 MB: 71 to 64 us).
+// With src the same for the wave and an offset a lane, and with an address a lane.
+__device__ __forceinline__ void stream_to_lds(const void* src, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+               :: "v"(offset), "s"(src), "s"(lds) : "m0", "memory");
+}
+__device__ __forceinline__ void stream_row_to_lds(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt"
+               :: "v"(src), "s"(lds) : "m0", "memory");
+}
+
 // 4 bytes per lane of the lower half-wave, to lds + 4 * lane.
 __device__ __forceinline__ void queue_words_to_lds(const void* src, uint32_t lds) {
   if (lane_here() < 32)
