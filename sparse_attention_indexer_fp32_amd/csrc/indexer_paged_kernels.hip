@@ -87,9 +87,9 @@ constexpr uint32_t kDropped = 0xFFFFFFFCu;
 // A workgroup's waves take 32 keys each of a tile of 128.  Keys go straight to LDS, in a ring of the wave's own, kDepth tiles
 // ahead and without a barrier: eight keys an instruction, whole rows.  (Loaded to
 // registers as the matrix instruction takes them, 16 of a row's bytes an instruction, 64
-// requests of 34816 keys took 71 us against TIME.)  WHOLE: every tile of 32 keys
+// requests of 34816 keys took 71 us against 60.)  WHOLE: every tile of 32 keys
 // lies in one page, and so in one piece of memory that the cache either holds or does not: one
-// scalar address for all of its loads (with an address a key, TIME).
+// scalar address for all of its loads (with an address a key 63 us).
 constexpr int kDepth = 2;
 constexpr int kFewTile = kWaves * kWaveKeys;
 constexpr int kKeyBytes = kWaveKeys * kDim;

@@ -146,6 +146,9 @@ int prefill_wgs(int cus, int32_t num_tokens, int32_t num_heads, int64_t num_kv, 
   return num_requests <= latent::kPlanRequests && pays ? (int)round : 0;
 }
 
+// Workgroups of a launch over shared prefixes: two run on a CU.
+int shared_wgs(int cus) { return 2 * cus; }
+
 topk_status_t check_queries(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const uint16_t* out,
                             int32_t num_tokens, int32_t num_heads, int width) {
   if (num_tokens < 0 || num_heads < 0) return invalid("num_tokens and num_heads must be >= 0");
@@ -411,7 +414,7 @@ topk_status_t latent_attention_shared_workspace(int32_t num_tokens, int32_t num_
   int cus = 0;
   const topk_status_t st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
-  *bytes = latent::shared_layout(latent::shared_tokens(num_tokens, num_heads, 0), num_heads, cus).total();
+  *bytes = latent::shared_layout(latent::shared_tokens(num_tokens, num_heads, 0), num_heads, shared_wgs(cus)).total();
   return TOPK_SUCCESS;
 }
 
@@ -446,7 +449,7 @@ topk_status_t latent_attention_shared(const uint16_t* q, int64_t q_token_stride,
   int cus = 0;
   st = device_cus(&cus);
   if (st != TOPK_SUCCESS) return st;
-  const latent::SplitLayout s = latent::shared_layout(at_once, num_heads, cus);
+  const latent::SplitLayout s = latent::shared_layout(at_once, num_heads, shared_wgs(cus));
   if (!workspace || workspace_bytes < s.total()) return invalid("the workspace is smaller than latent_attention_shared_workspace says");
   if (!aligned(workspace)) return invalid("the workspace must start on a 16-byte boundary");
   char* p = static_cast<char*>(workspace);
@@ -468,7 +471,7 @@ topk_status_t latent_attention_shared(const uint16_t* q, int64_t q_token_stride,
   a.out = out;
   a.lse = lse;
   a.num_heads = num_heads;
-  a.wgs = cus;
+  a.wgs = shared_wgs(cus);
   for (int64_t t = 0; t < num_tokens; t += at_once) {
     a.first_token = (int32_t)t;
     a.num_tokens = (int32_t)(num_tokens - t < at_once ? num_tokens - t : at_once);

@@ -134,7 +134,7 @@ hipError_t launch_attend(const AttendArgs& a, bool e4m3, hipStream_t stream);
 // second launch.  Tokens are taken `shared_tokens` at a time.
 constexpr int kUnitWaves = 4;
 constexpr int kUnitRows = 16 * kUnitWaves;
-constexpr int kSharedTiles = 4;      // tiles a workgroup takes at least
+constexpr int kSharedTiles = 6;      // tiles a workgroup takes at least, the cost of a unit among them
 struct SharedArgs {
   const uint16_t* q;
   int64_t q_token_stride, q_head_stride;   // elements

@@ -13,8 +13,15 @@
 // both units, and of as many more as the units were cut in.
 //
 // The tiling within a workgroup is the absorbed kernel's (attend_kernels.hip):
-// waves of 16 rows, tiles of 32 keys staged once for four waves, two rings of four
-// waves on alternate tiles.
+// waves of 16 rows, tiles of 32 keys staged once for four waves, and two workgroups on a CU, that
+// drift apart, so that one multiplies while the other waits.  (One workgroup of two rings, in step at every tile's
+// barrier, halves the parts: 64 requests x 32 heads behind 32768 positions 225 us against 213, 8 x 16 behind 4096
+// 35 and 29.  A workgroup of eight waves that deals the scores out by keys and the values by latents, so
+// that each byte of LDS is read half as often, needs two barriers a tile and the weights through LDS: 269.  Waves of 32 rows,
+// one to a SIMD, with the softmax step laid between matrix instructions: 245.)
+//
+// Measured (MI355X): 64 requests x 32 heads behind 32768 positions 207 us + 9 of the join, 715 TFLOP/s: the matrix
+// cores are busy 40 % of the time, and 15 % is waiting for rows (with all rows in L2: 181).  8 x 16 behind 4096 18 + 6 us.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -27,8 +34,12 @@
 namespace latent {
 namespace {
 
-constexpr int kRings = 2;
-constexpr int kThreads = 64 * kUnitWaves * kRings;
+constexpr int kThreads = 64 * kUnitWaves;
+
+// What a unit costs beside its tiles, in tiles: its rows, starts and first keys are waited for, its part is
+// written and read again.  (Counted by their tiles alone, the units of 64 requests with a single key each beside
+// a prefix of 32768 all fell to one workgroup: 652 us, and 200 so; 150 x 2 tokens of five groups 294 and 234.)
+constexpr uint32_t kUnitCost = 4;
 
 // The arguments, loaded anew: what is read through this does not stay in scalar registers, of which
 // the loop over the tiles has few to spare, from one use to the next.
@@ -99,9 +110,9 @@ __device__ __forceinline__ Entity entity(const SharedArgs& a, int e) {
   return u;
 }
 
-__device__ __forceinline__ uint32_t tiles_of(const Entity& u) {
+__device__ __forceinline__ uint32_t cost_of(const Entity& u) {
   const uint32_t n = ((uint32_t)u.keys + kTileKeys - 1) / kTileKeys;
-  return u.request >= 0 && n == 0 ? 1 : n;       // a request's rows are somebody's, with or without keys
+  return u.request >= 0 || n > 0 ? n + kUnitCost : 0;      // a request's rows are somebody's, with or without keys
 }
 __device__ __forceinline__ uint32_t blocks_of(const Entity& u) { return (uint32_t)((u.rows + kUnitRows - 1) / kUnitRows); }
 
@@ -150,15 +161,15 @@ __device__ __forceinline__ void clear_rows(uint32_t stage, int wave) {
 
 template <bool E4M3>
 __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
-  using L = Lds<kUnitWaves, kRings, E4M3>;
+  using L = Lds<kUnitWaves, 1, E4M3>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % kUnitWaves, ring = __builtin_amdgcn_readfirstlane(tid >> 6) / kUnitWaves;
-  const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + ring * L::kRingBytes;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int share = (int)blockIdx.x;
   auto weight = [&](int e) {
     const Entity u = entity(args_here(), e);
-    return blocks_of(u) * tiles_of(u);
+    return blocks_of(u) * cost_of(u);
   };
   // the plan is made where the rows go
   SharePlan& plan = *reinterpret_cast<SharePlan*>(lds);
@@ -175,10 +186,12 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
   while (lo < hi) {
     const SharedArgs a = args_here();
     const float scale_log2 = fabsf(a.scale_log2);
-    // the part [first, last) of the n tiles of a unit
+    // the part [first, last) of the tiles of a unit, whose own cost comes before them
     const Entity u = entity(a, e);
-    const uint32_t n = tiles_of(u), blocks = blocks_of(u), block = (lo - start) / n, begin = start + block * n;
-    const int first = (int)(lo - begin), last = (int)(hi - begin < n ? hi - begin : n);
+    const uint32_t n = cost_of(u), blocks = blocks_of(u), block = (lo - start) / n, begin = start + block * n;
+    const uint32_t until = hi - begin < n ? hi - begin : n;
+    const bool begins = lo == begin;
+    const int first = lo - begin > kUnitCost ? (int)(lo - begin - kUnitCost) : 0, last = until > kUnitCost ? (int)(until - kUnitCost) : 0;
     const int unit_row = u.row0 + (int)block * kUnitRows;
     const int unit_rows = u.rows - (int)block * kUnitRows < kUnitRows ? u.rows - (int)block * kUnitRows : kUnitRows;
     // Positions end where the request's last row of the unit does; `limit`, where this lane's row does.
@@ -201,8 +214,8 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
     int into = 0;                         // the stage of the tile to be queued next
     const uint32_t own_entries = lds_base + L::kEntries + wave * 256;
     const uint32_t scales = lds_base + L::kScales + wave * L::kStages * 128;
-    const int part_from = u.key0 + (first + ring) * kTileKeys;    // (keys end below 2^31, and no tile begins past them)
-    auto from_of = [&](int i) { return part_from + kRings * i * kTileKeys; };
+    const int part_from = u.key0 + first * kTileKeys;    // (keys end below 2^31, and no tile begins past them)
+    auto from_of = [&](int i) { return part_from + i * kTileKeys; };
     auto load_entries = [&](int i) {
       int pos = from_of(i) + (lane_here() & (kTileKeys - 1));
       pos = pos < end ? pos : end - 1;
@@ -210,9 +223,8 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
     };
     lds_barrier();                        // the plan's or the last part's reads are done
     const int used = end > u.key0 ? (int)(((uint32_t)(end - u.key0) + kTileKeys - 1) / kTileKeys) : 0;
-    const int tiles = (int)(used < last ? used : last) - first;
-    const int mine = __builtin_amdgcn_readfirstlane(tiles) - ring;             // this ring's are the i with kRings i < mine
-    if (mine > 0) load_entries(0);
+    const int tiles = __builtin_amdgcn_readfirstlane((used < last ? used : last) - first);
+    if (tiles > 0) load_entries(0);
 
     uint4 q[kLatentSteps + kRopeSteps];
     {
@@ -229,7 +241,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
       if (entry >= 0) at = ((int64_t)entry << a.log2_page) + (pos & ((1 << a.log2_page) - 1));
       const int slot = pos < end && at >= 0 && at < a.cache.num_slots ? (int)at : -1;
       mask = (uint32_t)__ballot(slot >= 0);
-      if (kRings * (i + 1) < mine) load_entries(i + 1);
+      if (i + 1 < tiles) load_entries(i + 1);
       if (E4M3) {
         const float* from = slot >= 0 ? a.cache.scale + slot : reinterpret_cast<const float*>(kZeroRow);
         queue_words_to_lds(from, scales + into * 128);
@@ -241,7 +253,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
 #pragma unroll
     for (int d = 0; d < L::kAhead; ++d) {
       masks[d] = 0;
-      if (kRings * d < mine) {
+      if (d < tiles) {
         queue(d, masks[d]);
         if (d + 1 < L::kAhead) wait_loads<L::kLoads>();        // the next entries
       }
@@ -256,15 +268,14 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
     for (int k = 0; k < kLatentSteps + kRopeSteps; ++k)
       st.q[k] = __builtin_bit_cast(bf16x8, make_uint4(q[k].x ^ sign, q[k].y ^ sign, q[k].z ^ sign, q[k].w ^ sign));
     int stage_at = 0;                     // the stage of the tile being computed
-    for (int i = 0; kRings * i < mine + ring; ++i) {
-      if (L::kAhead > 1 && kRings * (i + 1) < mine)
+    for (int i = 0; i < tiles; ++i) {
+      if (L::kAhead > 1 && i + 1 < tiles)
         wait_loads<L::kLoads>();          // all but the next tile's rows
       else
         wait_loads<0>();
       lds_barrier();            // every wave's rows are there, and nobody reads the stage before any more
-      const bool busy = kRings * i < mine && live_wave;        // (ring 1 may have none in the last round)
       masks[L::kAhead] = 0;
-      if (kRings * (i + L::kAhead) < mine) queue(i + L::kAhead, masks[L::kAhead]);
+      if (i + L::kAhead < tiles) queue(i + L::kAhead, masks[L::kAhead]);
       const int from = from_of(i);
       const uint32_t mask = masks[0] & below(limit, from);
 #pragma unroll
@@ -272,52 +283,39 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
       const uint32_t stage = lds_base + stage_at * L::kStageBytes, sc = scales + stage_at * 128;
       stage_at = stage_at + 1 < L::kStages ? stage_at + 1 : 0;
       f32x4 s[2];
-      if (busy) score_tile<E4M3>(st, s, stage, sc, reads, lane);
-      // (the same for all waves of the workgroup: either ring's tile)
-      if (least < end && least < part_from + (kRings * (i + 1) - ring) * kTileKeys) {
+      if (live_wave) score_tile<E4M3>(st, s, stage, sc, reads, lane);
+      // (the same for all waves of the workgroup)
+      if (least < end && least < part_from + (i + 1) * kTileKeys) {
         lds_barrier();
-        if (kRings * i < mine) clear_rows<E4M3>(stage, wave);
+        clear_rows<E4M3>(stage, wave);
         lds_barrier();
       }
-      if (busy) {
+      if (live_wave) {
         const bf16x8 p = weights_of_tile<E4M3, true>(st, s, sc, mask, scale_log2, lane);
         for_values<E4M3>(stage, reads, [&](int cb, bf16x8 cols) { st.o[cb] = mfma16(cols, p, st.o[cb]); });
       }
     }
 
-    // the second ring's waves hand theirs to the first's
-    f32x4* other_o = reinterpret_cast<f32x4*>(lds + wave * (kHeads * kLatent * 4)) + lane;
-    float2* other_ml = reinterpret_cast<float2*>(lds + kUnitWaves * (kHeads * kLatent * 4) + wave * 512) + lane;
-    lds_barrier();
-    if (ring > 0) {
-#pragma unroll
-      for (int cb = 0; cb < kColBlocks; ++cb) other_o[cb * 64] = st.o[cb];
-      *other_ml = make_float2(st.m, st.l);
-    }
-    lds_barrier();
     const SharedArgs after = args_here();
     const Entity v = entity(after, e);
     // this part's places: a unit's first part has its own, any other its share's
-    const int piece = first == 0 ? first_piece(after, v) + (int)block * kUnitWaves : 2 * after.pieces + share * kUnitWaves;
-    if (ring == 0 && live_wave) {
-      const float2 ml = *other_ml;
-      const float m = fmaxf(st.m, ml.x);
-      const float f = __builtin_amdgcn_exp2f(st.m - m), g = __builtin_amdgcn_exp2f(ml.x - m);
-      const float l = sum_of_4(st.l * f + ml.y * g);
+    const int piece = begins ? first_piece(after, v) + (int)block * kUnitWaves : 2 * after.pieces + share * kUnitWaves;
+    const float l = sum_of_4(st.l);       // this lane's row: its sum is spread over four lanes
+    if (live_wave) {
       const int64_t at = piece + wave;
       float* o = after.part_out + at * (kHeads * kLatent) + lane * 4;
 #pragma unroll
-      for (int cb = 0; cb < kColBlocks; ++cb) *reinterpret_cast<f32x4*>(o + cb * 256) = st.o[cb] * f + other_o[cb * 64] * g;
-      if (lane < kHeads) after.part_ml[at * kHeads + lane] = make_float2(m, l);
+      for (int cb = 0; cb < kColBlocks; ++cb) *reinterpret_cast<f32x4*>(o + cb * 256) = st.o[cb];
+      if (lane < kHeads) after.part_ml[at * kHeads + lane] = make_float2(st.m, l);
     }
-    if (first == 0 && tid < unit_rows) {
+    if (begins && tid < unit_rows) {
       const Shares shares(total, (uint32_t)after.wgs, kSharedTiles);
       const int parts = (int)shares.owner(begin + n - 1) - share + 1;
       int4* rec = after.part_rec + 2 * ((int64_t)unit_row + tid);
       rec[v.request >= 0 ? 1 : 0] = make_int4(piece + (tid >> 4), 2 * after.pieces + (share + 1) * kUnitWaves + (tid >> 4), parts, tid & 15);
       if (v.request >= 0 && v.key0 == 0) rec[0] = make_int4(0, 0, 0, 0);       // no shared prefix
     }
-    lo = begin + last;
+    lo = begin + until;
     if (block + 1 == blocks && lo == begin + n) {
       start += blocks * n;
       if (lo < hi) e = __builtin_amdgcn_readfirstlane(next_entity(weight, e + 1, after.num_groups + after.num_requests));
@@ -429,7 +427,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void shared_join_kernel(SharedArgs
 
 template <bool E4M3>
 hipError_t launch(const SharedArgs& a, hipStream_t stream) {
-  constexpr int kLds = Lds<kUnitWaves, kRings, E4M3>::kBytes;
+  constexpr int kLds = Lds<kUnitWaves, 1, E4M3>::kBytes;
   hipLaunchKernelGGL(shared_kernel<E4M3>, dim3((unsigned)a.wgs), dim3(kThreads), kLds, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -445,7 +443,7 @@ hipError_t launch(const SharedArgs& a, hipStream_t stream) {
 int shared_tokens(int num_tokens, int num_heads, int64_t keys) {
   int64_t n = 16384 / (num_heads / 8 + 2);
   n = n < 1 ? 1 : (n < num_tokens ? n : num_tokens);
-  const int64_t tiles = keys / kTileKeys + 2;
+  const int64_t tiles = keys / kTileKeys + 2 + kUnitCost;
   auto units = [&](int64_t t) { return 2 * (t * num_heads / kUnitRows + t + 1); };
   while (n > 1 && units(n) > (int64_t)INT32_MAX / tiles) n = (n + 1) / 2;
   return units(n) > (int64_t)INT32_MAX / tiles ? 0 : (int)n;
