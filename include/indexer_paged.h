@@ -23,7 +23,8 @@
  *     large in one of their elements over all;
  *   scale = max|y| / 448 (1 where y is all zero), codes = y / scale rounded to
  *     nearest even (what lies within two units of fp32 from a tie may go either way).
- *     A row with a NaN or an infinity has a NaN scale.
+ *     A row with a NaN or an infinity has a NaN scale, and so has one whose sums in the
+ *     mixing leave fp32 (values beyond 2^120).
  * cos_sin (max_positions, 64) fp32: the cosines of the 32 angles of a position, then
  * their sines; 16-byte aligned.  All arithmetic is fp32; each stored value is rounded once.
  *
@@ -131,7 +132,7 @@ topk_status_t indexer_cache_load_paged(const int32_t* page_table, const int32_t*
  * Rows from q_starts[num_requests] on are padding: their logits are left as
  * they are, and their lens are 0.  For topk_transform, a request's row of the page table
  * stands for each of its tokens.
- * num_tokens * (width / 64 + 1) must stay below 2^31, and width below 2^30.
+ * num_tokens * (width / 64 + 1) must stay below 2^31, and width below 2^29.
  */
 topk_status_t indexer_logits_paged(const uint8_t* q, const float* weights, const uint8_t* keys, int64_t key_stride,
                                    const float* key_scale, const int32_t* page_table, const int32_t* seq_lens,

@@ -206,7 +206,7 @@ topk_status_t indexer_logits_paged(const uint8_t* q, const float* weights, const
   topk_status_t st = check_paged(keys, key_stride, key_scale, num_slots, page_table, page_size, num_requests, pages_per_row, &a.cache);
   if (st != TOPK_SUCCESS) return st;
   if (num_tokens < 0) return invalid("num_tokens must be >= 0");
-  if (width < 0 || width >= (int64_t)1 << 30) return invalid("width must be in [0, 2^30)");
+  if (width < 0 || width >= (int64_t)1 << 29) return invalid("width must be in [0, 2^29)");
   if (num_tokens == 0) return TOPK_SUCCESS;
   if (!q || !weights || !q_starts) return invalid("q, weights and q_starts must be non-null");
   if (num_requests > 0 && !seq_lens) return invalid("seq_lens must be non-null");

@@ -129,7 +129,7 @@ def _logits(lib, **kw):
 
 @pytest.mark.parametrize("kw", BAD_KEYS + BAD_PAGES + [
     dict(q=None), dict(q=A + 4), dict(w=None), dict(w=A + 4), dict(seq=None), dict(qs=None), dict(out=None), dict(T=-1),
-    dict(width=-1), dict(width=2 ** 31), dict(T=2 ** 20, width=2 ** 20)])
+    dict(width=-1), dict(width=2 ** 29, T=1), dict(width=2 ** 31), dict(T=2 ** 20, width=2 ** 20)])
 def test_logits_refusals(lib, kw):
     assert _logits(lib, **kw) == 1 and topk.topk_last_error()
 
