@@ -111,6 +111,12 @@ __device__ __forceinline__ void queue_to_lds(const char* src, uint32_t lds) {
                :: "v"(src), "s"(lds) : "m0", "memory");
 }
 
+// With `src` the same for the wave, and an offset a lane.
+__device__ __forceinline__ void queue_to_lds(const char* src, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(offset), "s"(src), "s"(lds) : "m0", "memory");
+}
+
 // The same for bytes that are read once, by one workgroup: they are not kept in the caches (64 requests of
 // 34816 index keys, 290 MB: 71 to 64 us).
 // With src the same for the wave and an offset a lane, and with an address a lane.

@@ -159,6 +159,27 @@ __device__ __forceinline__ void clear_rows(uint32_t stage, int wave) {
   }
 }
 
+// The rows of codes of a wave's eight keys, where they lie in a row of slots from `slot` on: as load_tile, but with scalar
+// addresses that step from row to row and offsets of 32 bits (strides are at most kMaxStride).  Vector
+// instructions bound the kernel over codes, and addresses formed lane by lane are a sixth of them: 64
+// requests x 32 heads behind 32768 positions 251 us against 235.  (Rows of bf16 are bound elsewhere, and for them the same
+// took 231 us against 222, as it leaves too few scalar registers.)
+constexpr int kWaveRows = kTileKeys / kUnitWaves;
+constexpr int64_t kMaxStride = 1 << 24;
+__device__ __forceinline__ void load_codes(const Cache& c, int slot, uint32_t lds, int wave) {
+  const int lane = lane_here();
+  const char* row = c.latent + (int64_t)slot * c.latent_stride;
+  const uint32_t second = lane < 32 ? 0 : (uint32_t)c.latent_stride;      // two rows an instruction
+  const uint32_t chunk = ((lane & 31) ^ code_swizzle(wave * kWaveRows + (lane >> 5))) * 16;
+#pragma unroll
+  for (int i = 0; i < kWaveRows; i += 2)
+    queue_to_lds(row + i * c.latent_stride, (chunk ^ (uint32_t)(code_swizzle(i) * 16)) + second, lds + (wave * kWaveRows + i) * kLatent);
+  const int key = lane >> 3;
+  queue_to_lds(c.rope + (int64_t)slot * c.rope_stride,
+               (uint32_t)key * (uint32_t)c.rope_stride + ((lane ^ ((wave * kWaveRows + key) >> 1)) & 7) * 16,
+               lds + kTileCodes + wave * kWaveRows * kRopeBytes);
+}
+
 template <bool E4M3>
 __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
   using L = Lds<kUnitWaves, 1, E4M3>;
@@ -209,6 +230,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
       least = behind + first_token;
     }
     const bool live_wave = wave * 16 < unit_rows;
+    const bool near_rows = a.cache.latent_stride <= kMaxStride && a.cache.rope_stride <= kMaxStride;
 
     uint32_t masks[L::kAhead + 1];
     int into = 0;                         // the stage of the tile to be queued next
@@ -237,16 +259,22 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
     auto queue = [&](int i, uint32_t& mask) {
       const int entry = read_lds<int>(own_entries + (uint32_t)(i & 1) * 128 + (lane_here() & 31) * 4);
       const int pos = from_of(i) + (lane_here() & (kTileKeys - 1));
-      int64_t at = entry;
-      if (entry >= 0) at = ((int64_t)entry << a.log2_page) + (pos & ((1 << a.log2_page) - 1));
-      const int slot = pos < end && at >= 0 && at < a.cache.num_slots ? (int)at : -1;
+      // (a page beyond 2^31 slots, or a negative one, is not there either)
+      const int at = (int)(((uint32_t)entry << a.log2_page) + (uint32_t)(pos & ((1 << a.log2_page) - 1)));
+      const int slot = pos < end && (uint32_t)entry <= 0x7FFFFFFFu >> a.log2_page && at < (int)a.cache.num_slots ? at : -1;
       mask = (uint32_t)__ballot(slot >= 0);
       if (i + 1 < tiles) load_entries(i + 1);
       if (E4M3) {
         const float* from = slot >= 0 ? a.cache.scale + slot : reinterpret_cast<const float*>(kZeroRow);
         queue_words_to_lds(from, scales + into * 128);
       }
-      load_tile<kUnitWaves, E4M3>(a.cache, slot, lds_base + into * L::kStageBytes, wave);
+      // this wave's keys: all there, and in one page?
+      const int first_pos = from_of(i) + wave * kWaveRows;
+      if (E4M3 && near_rows && (mask >> (wave * kWaveRows) & 0xFF) == 0xFF &&
+          (first_pos >> a.log2_page) == ((first_pos + kWaveRows - 1) >> a.log2_page))
+        load_codes(a.cache, __builtin_amdgcn_readlane(slot, wave * kWaveRows), lds_base + into * L::kStageBytes, wave);
+      else
+        load_tile<kUnitWaves, E4M3>(a.cache, slot, lds_base + into * L::kStageBytes, wave);
       into = into + 1 < L::kStages ? into + 1 : 0;
     };
     wait_loads<kLatentSteps + kRopeSteps>();
