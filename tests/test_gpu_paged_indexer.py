@@ -301,6 +301,37 @@ def test_scores_are_those_of_contiguous_keys(lib, dev, new):
         assert torch.equal(got[t, :int(rows[t])], want[t, :int(rows[t])])
 
 
+@pytest.mark.parametrize("ps", [4, 32])
+@pytest.mark.parametrize("new", [1, 2, 6])
+def test_scores_of_pages_named_twice(lib, dev, new, ps):
+    """Requests that name one page several times, their own and each other's, have its scores as often; the width is wider
+    than what is cached."""
+    import torch
+    rng = np.random.default_rng(5)
+    keys = torch.from_numpy(_finite_codes(rng, (4 * ps, 128))).to(dev)
+    scale = torch.from_numpy(rng.uniform(0.5, 2, 4 * ps).astype(np.float32)).to(dev)
+    q1, w1 = _finite_codes(rng, (new, 32, 128)), rng.standard_normal((new, 32)).astype(np.float32)
+    q, w = torch.from_numpy(np.tile(q1, (2, 1, 1))).to(dev), torch.from_numpy(np.tile(w1, (2, 1))).to(dev)
+    table = _i32([[3, 1, 3, 3, 0], [3, 3, 1, 3, 1]], dev)
+    width = 5 * ps + 70
+    got, lens = lib.indexer_logits_paged(q, w, keys, scale, table, _i32([5 * ps, 5 * ps], dev), _i32([0, new, 2 * new], dev), ps,
+                                         width=width, out=torch.full((2 * new, width), float(GUARD), device=dev))
+    got = got.cpu().numpy()
+    assert lens.tolist() == [5 * ps - new + i + 1 for i in range(new)] * 2
+    for i in range(new):
+        a, b = got[i], got[new + i]
+        n = 5 * ps - new + i + 1
+        assert (a[n:] == GUARD).all() and (b[n:] == GUARD).all()
+        page = lambda row, p: row[p * ps:min(n, (p + 1) * ps)]     # noqa: E731
+        for row, p in ((a, 2), (b, 0), (b, 1), (b, 3)):
+            np.testing.assert_array_equal(page(row, p), page(a, 0)[:len(page(row, p))])
+        np.testing.assert_array_equal(page(a, 1), page(b, 2))
+        rows = np.arange(ps) + 3 * ps
+        want = ix.indexer_scores_row(q1[i], w1[i], keys.cpu().numpy()[rows], scale.cpu().numpy()[rows], range(ps))
+        err = check(f"{i}", a[:ps], want, ix.fp32_error_bound(q1[i], w1[i], keys.cpu().numpy()[rows], scale.cpu().numpy()[rows], range(ps)))
+        assert err is None, err
+
+
 def test_scores_far_slots(lib, dev):
     """Slots whose bytes lie beyond 2^32 of the cache's start."""
     import torch

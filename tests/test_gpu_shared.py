@@ -206,6 +206,28 @@ def test_strides_and_far_slots(lib, dev):
     _check_token("second", small, qh[1], np.arange(90), 0.1, _host(out)[1], _host(lse)[1])
 
 
+@pytest.mark.parametrize("slots,stride,rope_stride", [(70000, 65536, 32768), (300, 2 ** 24, 64), (300, 2 ** 24 + 16, 64), (2000, 512, 2 ** 20)])
+def test_codes_in_wide_rows(lib, dev, slots, stride, rope_stride):
+    """8-bit rows far apart, before and beyond the distance that offsets of 32 bits are used for."""
+    import torch
+    rng = np.random.default_rng(8)
+    small, ps = Cache(rng, 96, True, dev), 16
+    pages = np.array([slots // ps - 1, 2, slots // ps - 3, 0, 7, slots // ps - 2])
+    at = torch.from_numpy((pages[:, None] * ps + np.arange(ps)).reshape(-1)).to(dev)
+    latent = torch.empty((slots, stride), dtype=torch.uint8, device=dev)[:, :512]
+    rope = torch.empty((slots, rope_stride), dtype=torch.bfloat16, device=dev)[:, :64]
+    scale = torch.full((slots,), float("nan"), device=dev)
+    latent[at], rope[at], scale[at] = small.latent, small.rope, small.scale
+    q, qh = _bf(rng, (3, 20, 576), dev)
+    table = np.array([[pages[0], pages[1], -1, -1, -1], [pages[0], pages[1], pages[2], pages[3], -1], [-1, -1, pages[4], pages[5], -1]])
+    out, lse = lib.latent_attention_shared(q, latent, rope, _i32(table, dev), _i32([32, 64, 57], dev), _i32([0, 1, 2, 3], dev),
+                                           _i32([0, 3], dev), _i32([27], dev), ps, 0.1, scale=scale)
+    out, lse = _host(out), _host(lse)
+    own = [np.arange(32), np.arange(64), np.r_[np.arange(27), 64:64 + 57 - 32]]      # the last one's second page is missing
+    for b in range(3):
+        _check_token(f"request {b}", small, qh[b], own[b], 0.1, out[b], lse[b], [0, 7, 19])
+
+
 def test_captured_and_on_streams(lib, dev):
     """Replays on other inputs equal the eager result bit for bit (no atomics, a fixed
     order of sums); two graphs of one stream and calls on two streams share nothing."""
