@@ -40,6 +40,7 @@ CASES = {
     "many_idle": ([20] * 1500, [1 if i in (0, 700, 1499) else 0 for i in range(1500)], [0, 1499, 1500], [64, 10], 8, 16, 0),
     "launches": ([4 + i % 9 for i in range(8500)], [1] * 8500, [0, 3000, 8500], [40, 100], 1, 16, 2),      # more tokens than a launch takes
     "launches_wide": ([1 + i % 30 for i in range(1000)], [1] * 1000, [0, 1000], [70], 128, 16, 0),
+    "wider_prompts_in_two_launches": ([925, 40], [920, 30], [0, 2], [100], 128, 64, 1),      # of one request's tokens
 }
 
 
