@@ -11,9 +11,10 @@
 //     of them; the matrix cores bound it.
 // In both the workgroups share all requests' tiles evenly.
 //
-// Measured (MI355X), 64-position pages: one token of each of 64 requests behind 4096 to 65536 keys 56-60 us, 5.1-5.4
-// TB/s (a loop that only reads the same bytes: 44-50); one token behind 2^20 keys 26 us, 5.4 TB/s; 1024
-// tokens behind 65536 keys 447-490 us, 1130-1230 TFLOP/s, which is what a large library matrix product reaches less 10-20 %.
+// Measured (MI355X), 64-position pages: one token of each of 64 requests behind 4096 to 65536 keys
+// 56-60 us, 5.1-5.4 TB/s (a loop that only reads the same bytes: 44-50); one token behind 2^20 keys 26
+// us, 5.4 TB/s; 1024 tokens behind 65536 keys 447-490 us, 1130-1230 TFLOP/s, which is what a large
+// library matrix product reaches less 10-20 %.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -89,12 +90,12 @@ constexpr uint32_t kDropped = 0xFFFFFFFCu;
 
 // ---- few tokens a request ---------------------------------------------------------------------
 
-// A workgroup's waves take 32 keys each of a tile of 128.  Keys go straight to LDS, in a ring of the wave's own, kDepth tiles
-// ahead and without a barrier: eight keys an instruction, whole rows.  (Loaded to
-// registers as the matrix instruction takes them, 16 of a row's bytes an instruction, 64
-// requests of 34816 keys took 71 us against 60.)  WHOLE: every tile of 32 keys
-// lies in one page, and so in one piece of memory that the cache either holds or does not: one
-// scalar address for all of its loads (with an address a key 63 us).
+// A workgroup's waves take 32 keys each of a tile of 128.  Keys go straight to LDS, in a ring of the
+// wave's own, kDepth tiles ahead and without a barrier: eight keys an instruction, whole rows.  (Loaded
+// to registers as the matrix instruction takes them, 16 of a row's bytes an instruction, 64 requests of
+// 34816 keys took 71 us against 60.)  WHOLE: every tile of 32 keys lies in one page, and so in one
+// piece of memory that the cache either holds or does not: one scalar address for all of its loads
+// (with an address a key 63 us).
 constexpr int kDepth = 2;
 constexpr int kFewTile = kWaves * kWaveKeys;
 constexpr int kKeyBytes = kWaveKeys * kDim;

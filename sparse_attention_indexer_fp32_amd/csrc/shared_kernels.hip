@@ -12,16 +12,19 @@
 // parts over disjoint keys add up, so a row's result is the sum of its parts of
 // both units, and of as many more as the units were cut in.
 //
-// The tiling within a workgroup is the absorbed kernel's (attend_kernels.hip):
-// waves of 16 rows, tiles of 32 keys staged once for four waves, and two workgroups on a CU, that
-// drift apart, so that one multiplies while the other waits.  (One workgroup of two rings, in step at every tile's
-// barrier, halves the parts: 64 requests x 32 heads behind 32768 positions 225 us against 213, 8 x 16 behind 4096
-// 35 and 29.  A workgroup of eight waves that deals the scores out by keys and the values by latents, so
-// that each byte of LDS is read half as often, needs two barriers a tile and the weights through LDS: 269.  Waves of 32 rows,
-// one to a SIMD, with the softmax step laid between matrix instructions: 245.)
+// The tiling within a workgroup is the absorbed kernel's (attend_kernels.hip): waves of 16 rows, tiles
+// of 32 keys staged once for four waves, and two workgroups on a CU, that drift apart, so that one
+// multiplies while the other waits.  (One workgroup of two rings, in step at every tile's barrier,
+// halves the parts: 64 requests x 32 heads behind 32768 positions 225 us against 213, 8 x 16 behind
+// 4096 35 and 29.  A workgroup of eight waves that deals the scores out by keys and the values by
+// latents, so that each byte of LDS is read half as often, needs two barriers a tile and the weights
+// through LDS: 269.  Waves of 32 rows, one to a SIMD, with the softmax step laid between matrix
+// instructions: 245.)
 //
-// Measured (MI355X): 64 requests x 32 heads behind 32768 positions 207 us + 9 of the join, 715 TFLOP/s: the matrix
-// cores are busy 40 % of the time, and 15 % is waiting for rows (with all rows in L2: 181).  8 x 16 behind 4096 18 + 6 us.
+// Measured (MI355X): 64 requests x 32 heads behind 32768 positions 203 us + 15 of the join, up to 725
+// TFLOP/s: matrix instructions, vector instructions and LDS are busy for 44 to 47 % of the time each, at
+// the 1.7 GHz that the card holds, and 15 % is waiting for rows (with all rows in L2: 181).  8 x 16
+// behind 4096 20 + 5 us.  150 x 2 tokens x 20 heads over codes 225-237 us: vector instructions, 68 %.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -36,9 +39,10 @@ namespace {
 
 constexpr int kThreads = 64 * kUnitWaves;
 
-// What a unit costs beside its tiles, in tiles: its rows, starts and first keys are waited for, its part is
-// written and read again.  (Counted by their tiles alone, the units of 64 requests with a single key each beside
-// a prefix of 32768 all fell to one workgroup: 652 us, and 200 so; 150 x 2 tokens of five groups 294 and 234.)
+// What a unit costs beside its tiles, in tiles: its rows, starts and first keys are waited for, its
+// part is written and read again.  (Counted by their tiles alone, the units of 64 requests with a
+// single key each beside a prefix of 32768 all fell to one workgroup: 652 us, and 200 so; 150 x 2
+// tokens of five groups 294 and 234.)
 constexpr uint32_t kUnitCost = 4;
 
 // The arguments, loaded anew: what is read through this does not stay in scalar registers, of which
@@ -159,11 +163,12 @@ __device__ __forceinline__ void clear_rows(uint32_t stage, int wave) {
   }
 }
 
-// The rows of codes of a wave's eight keys, where they lie in a row of slots from `slot` on: as load_tile, but with scalar
-// addresses that step from row to row and offsets of 32 bits (strides are at most kMaxStride).  Vector
-// instructions bound the kernel over codes, and addresses formed lane by lane are a sixth of them: 64
-// requests x 32 heads behind 32768 positions 251 us against 235.  (Rows of bf16 are bound elsewhere, and for them the same
-// took 231 us against 222, as it leaves too few scalar registers.)
+// The rows of codes of a wave's eight keys, where they lie in a row of slots from `slot` on: as
+// load_tile, but with scalar addresses that step from row to row and offsets of 32 bits (strides are at
+// most kMaxStride).  Vector instructions bound the kernel over codes, and addresses formed lane by lane
+// are a sixth of them: 64 requests x 32 heads behind 32768 positions 251 us against 235.  (Rows of bf16
+// are bound elsewhere, and for them the same took 231 us against 222, as it leaves too few scalar
+// registers.)
 constexpr int kWaveRows = kTileKeys / kUnitWaves;
 constexpr int64_t kMaxStride = 1 << 24;
 __device__ __forceinline__ void load_codes(const Cache& c, int slot, uint32_t lds, int wave) {
@@ -351,10 +356,10 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
   }
 }
 
-// Joins a row's parts: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  As in the absorbed kernel's join, a
-// workgroup takes 16 rows and kJoinBlocks blocks of 16 latent values, its waves every
-// fourth part each, with kJoinAhead parts' loads in flight; but rows' parts lie in places of their
-// own, so every lane finds its row's.
+// Joins a row's parts: out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.  As in the absorbed
+// kernel's join, a workgroup takes 16 rows and kJoinBlocks blocks of 16 latent values, its waves every
+// fourth part each, with kJoinAhead parts' loads in flight; but rows' parts lie in places of their own,
+// so every lane finds its row's.
 constexpr int kJoinWaves = 4;
 constexpr int kJoinAhead = 4;
 constexpr int kJoinBlocks = 4;
