@@ -22,9 +22,9 @@
 // instructions: 245.)
 //
 // Measured (MI355X): 64 requests x 32 heads behind 32768 positions 203 us + 15 of the join, up to 725
-// TFLOP/s: matrix instructions, vector instructions and LDS are busy for 44 to 47 % of the time each, at
-// the 1.7 GHz that the card holds, and 15 % is waiting for rows (with one row for all, from L1: 181).  8 x 16
-// behind 4096 20 + 5 us.  150 x 2 tokens x 20 heads over codes 225-237 us: vector instructions, 68 %.
+// TFLOP/s: matrix instructions, vector instructions and LDS are busy for 44 to 47 % of the time each,
+// and 15 % is waiting for rows (with one row for all, from L1: 181).  8 x 16 behind 4096 20 + 5 us.
+// 150 x 2 tokens x 20 heads over codes 225-237 us: vector instructions, 68 %.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
