@@ -241,11 +241,13 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
     int into = 0;                         // the stage of the tile to be queued next
     const uint32_t own_entries = lds_base + L::kEntries + wave * 256;
     const uint32_t scales = lds_base + L::kScales + wave * L::kStages * 128;
-    const int part_from = u.key0 + first * kTileKeys;    // (keys end below 2^31, and no tile begins past them)
-    auto from_of = [&](int i) { return part_from + i * kTileKeys; };
+    // Tiles begin below 2^31, but the last one may reach past it: positions of single keys are unsigned.
+    // (`end` is above 0 wherever there are tiles.)
+    const uint32_t part_from = (uint32_t)u.key0 + (uint32_t)first * kTileKeys;
+    auto from_of = [&](int i) { return (int)(part_from + (uint32_t)i * kTileKeys); };
     auto load_entries = [&](int i) {
-      int pos = from_of(i) + (lane_here() & (kTileKeys - 1));
-      pos = pos < end ? pos : end - 1;
+      uint32_t pos = (uint32_t)from_of(i) + (lane_here() & (kTileKeys - 1));
+      pos = pos < (uint32_t)end ? pos : (uint32_t)end - 1;
       queue_words_to_lds(list + (pos >> a.log2_page), own_entries + (uint32_t)(i & 1) * 128);
     };
     lds_barrier();                        // the plan's or the last part's reads are done
@@ -263,10 +265,10 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
     }
     auto queue = [&](int i, uint32_t& mask) {
       const int entry = read_lds<int>(own_entries + (uint32_t)(i & 1) * 128 + (lane_here() & 31) * 4);
-      const int pos = from_of(i) + (lane_here() & (kTileKeys - 1));
+      const uint32_t pos = (uint32_t)from_of(i) + (lane_here() & (kTileKeys - 1));
       // (a page beyond 2^31 slots, or a negative one, is not there either)
-      const int at = (int)(((uint32_t)entry << a.log2_page) + (uint32_t)(pos & ((1 << a.log2_page) - 1)));
-      const int slot = pos < end && (uint32_t)entry <= 0x7FFFFFFFu >> a.log2_page && at < (int)a.cache.num_slots ? at : -1;
+      const int at = (int)(((uint32_t)entry << a.log2_page) + (pos & ((1u << a.log2_page) - 1)));
+      const int slot = pos < (uint32_t)end && (uint32_t)entry <= 0x7FFFFFFFu >> a.log2_page && at < (int)a.cache.num_slots ? at : -1;
       mask = (uint32_t)__ballot(slot >= 0);
       if (i + 1 < tiles) load_entries(i + 1);
       if (E4M3) {
@@ -317,8 +319,9 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
       stage_at = stage_at + 1 < L::kStages ? stage_at + 1 : 0;
       f32x4 s[2];
       if (live_wave) score_tile<E4M3>(st, s, stage, sc, reads, lane);
-      // (the same for all waves of the workgroup)
-      if (least < end && least < part_from + (i + 1) * kTileKeys) {
+      // (the same for all waves of the workgroup; rows of a unit end within 64 positions, so the difference
+      // is a small one or positive)
+      if (least < end && least - from < kTileKeys) {
         lds_barrier();
         clear_rows<E4M3>(stage, wave);
         lds_barrier();

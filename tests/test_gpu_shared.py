@@ -347,3 +347,33 @@ def test_workspace_grows_with_tokens(lib, dev):
         assert n.value >= last
         last = n.value
     assert last < 2 ** 30
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("prefix", [1, 32, 0])
+def test_positions_up_to_the_last(lib, dev, e4m3, prefix):
+    """A request of 2^31 - 1 positions, of which a few pages exist, at both ends.  Behind a prefix of one position its
+    last tile reaches past 2^31; of its two tokens only the second attends the last position, which is not finite."""
+    import torch
+    rng = np.random.default_rng(14)
+    ps, H, n = 1024, 16, 2 ** 31 - 1
+    P = 2 ** 31 // ps
+    cache = Cache(rng, 3 * ps, e4m3, dev)
+    table = np.full((1, P), -1, np.int32)
+    table[0, 0], table[0, P - 1] = 1, 2                    # slots 1024 to 2047, and from 2048 on
+    last = 2 * ps + (n - 1) % ps                           # the last position's slot
+    q, qh = _bf(rng, (2, H, 576), dev)
+    note(f"far positions e4m3={e4m3} prefix={prefix}")
+    args = (q, cache.latent, cache.rope, _i32(table, dev), _i32([n], dev), _i32([0, 2], dev), _i32([0, 1], dev),
+            _i32([prefix], dev), ps, 0.05)
+    out, lse = lib.latent_attention_shared(*args, scale=cache.scale)
+    out, lse = _host(out), _host(lse)
+    for i in range(2):
+        _check_token(f"token {i}", cache, qh[i], np.arange(ps, last + i), 0.05, out[i], lse[i], (0, 7, 15))
+    cache.poison([last])
+    cache.poison(range(last + 1, 3 * ps))
+    cache.poison(range(ps))
+    out, lse = lib.latent_attention_shared(*args, scale=cache.scale)
+    out, lse = _host(out), _host(lse)
+    _check_token("before the last", cache, qh[0], np.arange(ps, last), 0.05, out[0], lse[0], (0, 7, 15))
+    assert np.isnan(out[1]).all() and np.isnan(lse[1]).all()
