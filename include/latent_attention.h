@@ -167,7 +167,8 @@ topk_status_t latent_cache_load_paged(const int32_t* page_table, const int32_t* 
  * cache holds in slots that are not selected is never used, NaN included.  A
  * selected row that makes a head's score NaN (the NaN scale of an E4M3 row
  * among others) or +inf makes that head's out and lse NaN; a score of -inf
- * weighs nothing.
+ * weighs nothing (its row takes part as 0 times its values: one that is infinite itself makes that
+ * element of out NaN, and lse stays as it is).
  * Scores, statistics and sums are fp32; the weights are rounded to bf16 for
  * the matrix cores, and the result once at the end.
  * Any score that is finite in fp32 counts as what it is.  Weights are as large as

@@ -132,22 +132,25 @@ __device__ __forceinline__ uint32_t below(int limit, int from) {
   return n >= kTileKeys ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1;
 }
 
-// Clears a stage's rows that hold an infinity or a NaN, eight rows a wave.  For tiles
-// whose keys count for some of the unit's rows only: one that leaves a key out has a weight of
-// 0 for it, but 0 times an infinity is not 0.  For rows that such a key
-// counts for nothing is lost: their scores are computed, and are not finite themselves (a
-// product with an infinity or a NaN in it never is), and so their sums and results are NaN already.
+// A tile whose keys count for some of the unit's rows only: a row that leaves a key out has a weight of 0
+// for it, but 0 times an infinity is not 0, so rows of the cache that hold an infinity or a NaN are
+// cleared.  What a row that does attend such a key has from it is kept: its score is never finite itself (a
+// product with an infinity or a NaN in it is not).  Is it NaN or +inf, so is the row's sum, and with it all of the
+// row's result.  Is it -inf, the key's weight is 0, and its row takes part as 0 times its values: where they
+// are not finite that is NaN, added here, and nothing elsewhere, as in tiles that all rows attend whole.
+// (Codes stand for no infinities, and a NaN among them gives a score of NaN.)
+
+// Rows of the stage that hold one, eight rows a wave, as bits from this wave's first row on.
 template <bool E4M3>
-__device__ __forceinline__ void clear_rows(uint32_t stage, int wave) {
+__device__ __forceinline__ uint32_t rows_not_finite(uint32_t stage, int wave) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  typedef __attribute__((address_space(3))) u32x4* lds_ptr;
   const int lane = lane_here();
   constexpr int kBytes = E4M3 ? kLatent : kRowBytes;
+  uint32_t rows = 0;
   for (int i = 0; i < kTileKeys / kUnitWaves; ++i) {
-    const uint32_t at = stage + (wave * (kTileKeys / kUnitWaves) + i) * kBytes + lane * 16;
     bool bad = false;
     if (lane * 16 < kBytes) {
-      const u32x4 w = read_lds<u32x4>(at);
+      const u32x4 w = read_lds<u32x4>(stage + (wave * (kTileKeys / kUnitWaves) + i) * kBytes + lane * 16);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (E4M3) {
@@ -159,8 +162,42 @@ __device__ __forceinline__ void clear_rows(uint32_t stage, int wave) {
         }
       }
     }
-    if (__any(bad) && lane * 16 < kBytes) *(lds_ptr)at = u32x4{};
+    rows |= (uint32_t)__any(bad) << i;
   }
+  return rows;
+}
+
+// 0 times the values of the stage's rows `rows` (bf16), added to the accumulators of the lanes whose
+// row attends them.
+__device__ __forceinline__ void add_nothing(HeadState& st, uint32_t stage, uint32_t rows, uint32_t mask) {
+  const int lane = lane_here(), g = lane >> 4;
+  for (; rows; rows &= rows - 1) {
+    const int key = __builtin_ctz(rows);
+    const uint32_t attends = (mask >> key & 1) ? 0xFFFFFFFFu : 0u;
+    const uint32_t at = stage + key * kRowBytes + (((g >> 1) ^ swizzle(key)) << 4) + (g & 1) * 8;
+#pragma unroll
+    for (int cb = 0; cb < kColBlocks; ++cb) {
+      const u32x2 v = read_lds<u32x2>((at ^ (uint32_t)((cb & 7) << 5)) + (cb >> 3) * 256);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t bits = (r & 1 ? v[r >> 1] & 0xFFFF0000u : v[r >> 1] << 16) & attends;
+        st.o[cb][r] = fmaf(__uint_as_float(bits), 0.f, st.o[cb][r]);
+      }
+      __builtin_amdgcn_sched_barrier(0);     // reads ahead would take registers that the loop has not
+    }
+  }
+}
+
+// Clears this wave's rows among `rows`.
+template <bool E4M3>
+__device__ __forceinline__ void clear_rows(uint32_t stage, int wave, uint32_t rows) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) u32x4* lds_ptr;
+  const int lane = lane_here();
+  constexpr int kBytes = E4M3 ? kLatent : kRowBytes;
+  for (uint32_t own = rows >> (wave * (kTileKeys / kUnitWaves)) & ((1u << (kTileKeys / kUnitWaves)) - 1); own; own &= own - 1)
+    if (lane * 16 < kBytes)
+      *(lds_ptr)(stage + (wave * (kTileKeys / kUnitWaves) + __builtin_ctz(own)) * kBytes + lane * 16) = u32x4{};
 }
 
 // The rows of codes of a wave's eight keys, where they lie in a row of slots from `slot` on: as
@@ -188,6 +225,7 @@ __device__ __forceinline__ void load_codes(const Cache& c, int slot, uint32_t ld
 template <bool E4M3>
 __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
   using L = Lds<kUnitWaves, 1, E4M3>;
+  typedef __attribute__((address_space(3))) uint8_t* byte_ptr;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -208,7 +246,7 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
   const uint32_t hi = __builtin_amdgcn_readfirstlane(plan.end);
   int e = __builtin_amdgcn_readfirstlane(plan.entity);
 
-  const TileReads reads = tile_reads<E4M3>(lane);
+  const TileReads whole_reads = tile_reads<E4M3>(lane);
   while (lo < hi) {
     const SharedArgs a = args_here();
     const float scale_log2 = fabsf(a.scale_log2);
@@ -317,14 +355,23 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedArgs) {
       for (int d = 0; d < L::kAhead; ++d) masks[d] = masks[d + 1];
       const uint32_t stage = lds_base + stage_at * L::kStageBytes, sc = scales + stage_at * 128;
       stage_at = stage_at + 1 < L::kStages ? stage_at + 1 : 0;
+      // (over codes formed anew: kept, they would be spilled, and a reload waits for all rows on their way)
+      const TileReads reads = E4M3 ? tile_reads<E4M3>(lane_here()) : whole_reads;
       f32x4 s[2];
       if (live_wave) score_tile<E4M3>(st, s, stage, sc, reads, lane);
       // (the same for all waves of the workgroup; rows of a unit end within 64 positions, so the difference
       // is a small one or positive)
       if (least < end && least - from < kTileKeys) {
-        lds_barrier();
-        clear_rows<E4M3>(stage, wave);
-        lds_barrier();
+        const uint32_t own = rows_not_finite<E4M3>(stage, wave);
+        if (lane == 0) *(byte_ptr)(lds_base + L::kBytes + wave) = (uint8_t)own;
+        lds_barrier();          // (all scores are computed, and the bytes read at the tile before are)
+        const uint32_t rows = __builtin_amdgcn_readfirstlane(read_lds<uint32_t>(lds_base + L::kBytes));
+        if (rows) {
+          if (!E4M3 && live_wave) add_nothing(st, stage, rows, mask);
+          lds_barrier();
+          clear_rows<E4M3>(stage, wave, rows);
+          lds_barrier();
+        }
       }
       if (live_wave) {
         const bf16x8 p = weights_of_tile<E4M3, true>(st, s, sc, mask, scale_log2, lane);
@@ -463,7 +510,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void shared_join_kernel(SharedArgs
 
 template <bool E4M3>
 hipError_t launch(const SharedArgs& a, hipStream_t stream) {
-  constexpr int kLds = Lds<kUnitWaves, 1, E4M3>::kBytes;
+  constexpr int kLds = Lds<kUnitWaves, 1, E4M3>::kBytes + 16;      // the ring, a byte of bits a wave
+  static_assert(kUnitWaves == 4 && kTileKeys == 8 * kUnitWaves, "a word of bits");
+  static_assert(2 * (kLds + 1280) <= 160 * 1024, "two workgroups to a CU");
   hipLaunchKernelGGL(shared_kernel<E4M3>, dim3((unsigned)a.wgs), dim3(kThreads), kLds, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -377,3 +377,58 @@ def test_positions_up_to_the_last(lib, dev, e4m3, prefix):
     out, lse = _host(out), _host(lse)
     _check_token("before the last", cache, qh[0], np.arange(ps, last), 0.05, out[0], lse[0], (0, 7, 15))
     assert np.isnan(out[1]).all() and np.isnan(lse[1]).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("name", ["several", "prompts", "decode", "heads_128"])
+def test_a_score_of_minus_infinity_weighs_nothing(lib, dev, e4m3, name):
+    """An infinite value in the row of a request's last position, which some of its tokens attend, all, or one alone
+    (bf16; an 8-bit row has it in its rotary part): heads whose score is -inf are as without the row, but for 0 times the infinity in
+    its own element, whoever shares their tile; heads whose score is +inf are NaN, and tokens before it are as without."""
+    import torch
+    x = Batch(name, e4m3, dev)
+    hit = [b for b in range(x.B) if x.new[b] and x.own[b] and len(x.slots(b, int(x.lens[b])))]
+    column = 100
+    for b in hit:
+        pos = int(x.lens[b]) - 1
+        slot = int(x.table[b][pos // x.ps]) * x.ps + pos % x.ps
+        if e4m3:
+            x.cache.rope[slot, 3] = float("inf")
+        else:
+            x.cache.latent[slot, column] = float("inf")
+    note(f"minus infinity e4m3={e4m3} {name}")
+    out, lse = x.run(lib)
+    torch.cuda.synchronize()
+    out, lse = _host(out), _host(lse)
+    seen = 0
+    for b in hit:
+        n, first, z = int(x.lens[b]), int(x.starts[b]), int(x.starts[b + 1]) - 1
+        up = x.qh[z, :, 515 if e4m3 else column] > 0
+        assert np.isnan(out[z][up]).all() and np.isnan(lse[z][up]).all()
+        heads = np.nonzero(~up)[0][:6]
+        got = out[z].copy()
+        if not e4m3:
+            assert np.isnan(got[~up][:, column]).all()
+        # the key's row counts for the weights of no head here; its own element is compared apart
+        slots = x.slots(b, n - 1)
+        for h in heads:
+            keys = np.concatenate([x.cache.c[slots], x.cache.r[slots]], 1)
+            a = lo.attend(x.qh[z, h], keys, x.cache.c[slots], 0.08)
+            rest = np.ones(512, bool)
+            rest[column] = e4m3
+            for err in (lo.check(f"{b} {h} out", got[h, rest], a.out[rest], a.out_bound[rest]),
+                        lo.check(f"{b} {h} lse", lse[z, h], a.lse, a.lse_bound)):
+                assert err is None, err
+            seen += 1
+        for t in range(max(first, z - 3), z):
+            _check_token(f"request {b} before", x.cache, x.qh[t], x.slots(b, n - (z - t)), 0.08, out[t], lse[t], (0, x.H - 1))
+    assert seen > 0
+    # and where nothing is shared, the results of the call over whole sequences
+    none = dict(x.args, group_starts=_i32([0], dev), shared_lens=_i32([], dev))
+    args = (x.q, x.cache.latent, x.cache.rope)
+    a, al = lib.latent_attention_shared(*args, softmax_scale=0.08, scale=x.cache.scale, **none)
+    none.pop("group_starts"), none.pop("shared_lens")
+    w, wl = lib.latent_attention_paged(*args, softmax_scale=0.08, scale=x.cache.scale, **none)
+    k = int(x.starts[-1])
+    assert torch.equal(torch.isnan(a[:k]), torch.isnan(w[:k])) and torch.equal(torch.isnan(al[:k]), torch.isnan(wl[:k]))
+    assert bool(torch.isnan(a[:k]).any())
