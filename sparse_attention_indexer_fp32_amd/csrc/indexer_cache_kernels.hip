@@ -133,7 +133,7 @@ __device__ __forceinline__ void mix(int l, Row& r) {
 // magnitude is an integer maximum of the bits without the sign: infinities and
 // NaN come out on top, and such a row's scale is NaN.  The codes are the row times the
 // reciprocal of its step, which moves what lies within two units of fp32 from a tie.  A step that is
-// subnormal would have no finite reciprocal: rows below 448 * 2^-126 take the smallest normal one.
+// subnormal would have no finite reciprocal, and a scale that is loses digits: a row's scale is 2^-126 at least.
 __device__ __forceinline__ float quantise(const Row& r, float factor, uint2 (&codes)[kChunks]) {
   uint32_t top = 0;
 #pragma unroll
@@ -141,10 +141,11 @@ __device__ __forceinline__ float quantise(const Row& r, float factor, uint2 (&co
   top = max_u32(top, dpp<kXor1>(top));
   top = max_u32(top, dpp<kXor2>(top));
   const float amax = __uint_as_float(top);
-  const float step = amax == 0.f                             ? 1.0f
-                     : !(amax < INFINITY)                     ? __uint_as_float(0x7FC00000u)
-                     : amax < 448.0f * 1.17549435e-38f ? 1.17549435e-38f
-                                                              : amax / 448.0f;
+  const float least = 0x1p-126f / factor;
+  const float step = amax == 0.f                  ? 1.0f
+                     : !(amax < INFINITY)         ? __uint_as_float(0x7FC00000u)
+                     : amax < 448.0f * least ? least
+                                                  : amax / 448.0f;
   const float inv = 1.0f / step;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {

@@ -490,3 +490,37 @@ def test_refusals(lib, dev):
                 dict(lens=t(3, dtype=i32)), dict(out=t(2, 64, dtype=bf))):
         with pytest.raises(ValueError):
             lib.indexer_logits_paged(**{**score, **bad})
+
+
+# ---- rows at the ends of the range --------------------------------------------------------------
+
+@pytest.mark.parametrize("mix", [False, True])
+def test_rows_far_below_one(lib, dev, mix):
+    """Down to values that are subnormal themselves, a row's scale is its maximum's part, 2^-126 at least, and its codes are
+    within half a step of it.  (No absolute term in the bounds: a row of zeros would not pass.)"""
+    import torch
+    rng = np.random.default_rng(21)
+    sizes = [1e-28, 1e-30, 1e-33, 1e-35, 3e-36, 3e-37, 1e-37, 1e-38, 1e-39, 2e-40]
+    k = (torch.from_numpy(rng.standard_normal((len(sizes), 128))) * torch.tensor(sizes, dtype=torch.float64)[:, None]).bfloat16()
+    kh = k.double().numpy()
+    least, clamped = 2.0 ** -126, 0
+    keys, scale = torch.zeros((16, 128), dtype=torch.uint8, device=dev), torch.zeros(16, device=dev)
+    q = k[:, None].expand(-1, 32, -1).contiguous().to(dev)
+    lib.indexer_cache_store(k.to(dev), _i32(range(len(sizes)), dev), keys, scale, hadamard=mix)
+    qc, qw = lib.indexer_queries(q, torch.ones((len(sizes), 32), device=dev), hadamard=mix)
+    codes, s = keys.cpu().numpy(), scale.double().cpu().numpy()
+    assert torch.equal(qc[:, 31], keys[:len(sizes)]) and torch.equal(qw[:, 31], scale[:len(sizes)])
+    for t in range(len(sizes)):
+        r = po.row(kh[t], mix=mix)
+        top = np.abs(r.y).max()
+        want = max(top / 448.0, least)
+        clamped += want == least
+        # the row's own error, the quotient's rounding and, with mixing, the product's and the factor's
+        off = r.slack.max() / 448.0 + 4 * po.U32 * want
+        assert abs(s[t] - want) <= off, (t, s[t], want, off)
+        bound = po.U8 * (np.abs(r.y) + r.slack) + po.TINY8 * s[t] + r.slack + 8 * po.U32 * np.abs(r.y)
+        err = check(f"row {t}", e4m3_value(codes[t]) * s[t], r.y, bound)
+        assert err is None, err
+        if top > 0.01 * least:
+            assert codes[t].any()
+    assert clamped >= 3
