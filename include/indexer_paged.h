@@ -21,9 +21,9 @@
  *   mixing (with hadamard != 0): y[i] = sum_j (-1)^popcount(i & j) x[j] / sqrt(128),
  *     which leaves products of a query and a key as they are and spreads what is
  *     large in one of their elements over all;
- *   scale = max|y| / 448, but 2^-126 at least (1 where y is all zero), codes = y / scale rounded to
- *     nearest even (what lies within two units of fp32 from a tie may go either way).
- *     A row with a NaN or an infinity has a NaN scale, and so has one whose sums in the
+ *   scale = max|y| / 448, but 2^-126 at least (1 where y is all zero), codes = y / scale, a quotient in
+ *     fp32 (with mixing, of numerator and denominator without their factor 1 / sqrt(128)), rounded to
+ *     nearest even.  A row with a NaN or an infinity has a NaN scale, and so has one whose sums in the
  *     mixing leave fp32 (values beyond 2^120).
  * cos_sin (max_positions, 64) fp32: the cosines of the 32 angles of a position, then
  * their sines; 16-byte aligned.  All arithmetic is fp32; each stored value is rounded once.

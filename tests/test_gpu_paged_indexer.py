@@ -524,3 +524,28 @@ def test_rows_far_below_one(lib, dev, mix):
         if top > 0.01 * least:
             assert codes[t].any()
     assert clamped >= 3
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -10, 1.0, 2.0 ** 100])
+def test_codes_of_ties(lib, dev, size):
+    """Codes are the fp32 quotient by the step, rounded to nearest even: exactly, where many values lie on ties
+    of the codes or one unit of fp32 beside one."""
+    import torch
+    rng = np.random.default_rng(22)
+    top = (1 + np.arange(128) / 128.0).astype(np.float32)         # every bf16 mantissa as a row's maximum
+    k = np.zeros((128, 128), np.float32)
+    # the bf16 numbers around the ties (an odd number of sixteenths, 16 to 32 of them) of a row
+    for t in range(128):
+        ties = np.array([(16 + 2 * (i % 8) + 1) * 2.0 ** (4 - i // 8) for i in range(126)]) % 448 * top[t] / 448
+        near = torch.from_numpy(ties).bfloat16().float().numpy()
+        k[t] = np.concatenate([[top[t]], near, [0.75 * top[t]]])
+    k = torch.from_numpy((k * rng.choice([-1, 1], k.shape) * size).astype(np.float32)).bfloat16()
+    v = k.float()
+    step = v.abs().amax(1) / 448                                  # fp32 divisions, as the definition's
+    want = (v / step[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    keys, scale = torch.zeros((128, 128), dtype=torch.uint8, device=dev), torch.zeros(128, device=dev)
+    lib.indexer_cache_store(k.to(dev), _i32(range(128), dev), keys, scale)
+    assert torch.equal(scale.cpu(), step)
+    assert torch.equal(keys.cpu(), want)
+    codes, w = lib.indexer_queries(k[:, None].expand(-1, 32, -1).contiguous().to(dev), torch.ones((128, 32), device=dev))
+    assert torch.equal(codes[:, 5].cpu(), want) and torch.equal(w[:, 31].cpu(), step)
