@@ -183,6 +183,22 @@ __device__ __forceinline__ int64_t workgroup() { return (int64_t)blockIdx.y * gr
 
 // ---- keys -------------------------------------------------------------------------------------
 
+// Takes a row's mean from its values, and returns its variance.  Two passes over the registers: the variance of values
+// far from 0 keeps its digits.
+__device__ __forceinline__ float centre(Row& y) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8 * kChunks; ++i) sum += y.v[i];
+  const float mean = quad_sum(sum) * (1.0f / kDim);
+  float sq = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8 * kChunks; ++i) {
+    y.v[i] -= mean;
+    sq = fmaf(y.v[i], y.v[i], sq);
+  }
+  return quad_sum(sq) * (1.0f / kDim);
+}
+
 __global__ __launch_bounds__(kThreads) void key_store_kernel(StoreArgs a) {
   const int l = threadIdx.x & (kLanes - 1);
   const int64_t t = workgroup() * kRowsPerWg + threadIdx.x / kLanes;
@@ -206,18 +222,18 @@ __global__ __launch_bounds__(kThreads) void key_store_kernel(StoreArgs a) {
     load_angles(a.turn, pos, l, angles);
   }
   if (a.norm_weight) {
-    // two passes over the registers: the variance of values far from 0 keeps its digits
-    float sum = 0.f;
+    float var = centre(y);
+    float eps = a.eps;
+    if (!(var < INFINITY)) {
+      // values beyond 2^60, whose squares leave fp32: the same of the row divided by 2^70 (the lanes of a
+      // row together; one that is not finite comes out as NaN)
+      load_row(a.k + t * a.k_stride, l, y);
 #pragma unroll
-    for (int i = 0; i < 8 * kChunks; ++i) sum += y.v[i];
-    const float mean = quad_sum(sum) * (1.0f / kDim);
-    float sq = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8 * kChunks; ++i) {
-      y.v[i] -= mean;
-      sq = fmaf(y.v[i], y.v[i], sq);
+      for (int i = 0; i < 8 * kChunks; ++i) y.v[i] *= 0x1p-70f;
+      var = centre(y);
+      eps *= 0x1p-140f;
     }
-    const float inv = 1.0f / sqrtf(quad_sum(sq) * (1.0f / kDim) + a.eps);
+    const float inv = 1.0f / sqrtf(var + eps);
 #pragma unroll
     for (int i = 0; i < 8 * kChunks; ++i) y.v[i] = fmaf(y.v[i] * inv, w.v[i], bias.v[i]);
   }

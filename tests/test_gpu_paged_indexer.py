@@ -549,3 +549,24 @@ def test_codes_of_ties(lib, dev, size):
     assert torch.equal(keys.cpu(), want)
     codes, w = lib.indexer_queries(k[:, None].expand(-1, 32, -1).contiguous().to(dev), torch.ones((128, 32), device=dev))
     assert torch.equal(codes[:, 5].cpu(), want) and torch.equal(w[:, 31].cpu(), step)
+
+
+@pytest.mark.parametrize("mix", [False, True])
+def test_norm_of_large_values(lib, dev, mix):
+    """The layer norm of rows up to the largest bf16 numbers, whose squares and sums do not fit fp32."""
+    import torch
+    rng = np.random.default_rng(23)
+    sizes = [1e3, 1e15, 2e18, 1e19, 1e20, 1e30, 1e36, 8e37, 1e38, 1e38]
+    k = (torch.from_numpy(rng.standard_normal((len(sizes), 128))).clamp(-3, 3)
+         * torch.tensor(sizes, dtype=torch.float64)[:, None]).bfloat16()
+    k[8] = k[8].abs()                                             # a sum beyond fp32
+    k[9, 77] = float("inf")
+    kh = k.double().numpy()
+    w, bias = 1 + 0.2 * torch.randn(128, generator=torch.Generator().manual_seed(3)), torch.full((128,), 0.1)
+    keys, scale = torch.zeros((16, 128), dtype=torch.uint8, device=dev), torch.zeros(16, device=dev)
+    lib.indexer_cache_store(k.to(dev), _i32(range(len(sizes)), dev), keys, scale, norm_weight=w.to(dev), norm_bias=bias.to(dev),
+                            eps=1e-6, hadamard=mix)
+    codes, s = keys.cpu().numpy(), scale.cpu().numpy()
+    for t in range(len(sizes) - 1):
+        _check_row(f"row {t}", kh[t], codes[t], s[t], weight=w.double().numpy(), bias=bias.double().numpy(), eps=1e-6, mix=mix)
+    assert np.isnan(s[len(sizes) - 1])
