@@ -232,10 +232,21 @@ __global__ __launch_bounds__(kStoreThreads) void store_kernel(StoreArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = (float)c[i];
   if (a.norm_weight) {
-    float sq = 0.f;
+    auto mean_square = [&] {
+      float sq = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
-    const float inv = 1.0f / sqrtf(wave_sum_f32(sq) * (1.0f / kLatent) + a.eps);
+      for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
+      return wave_sum_f32(sq) * (1.0f / kLatent);
+    };
+    float ms = mean_square(), eps = a.eps;
+    if (!(ms < INFINITY)) {
+      // values beyond 2^59, whose squares leave fp32: the same of the row divided by 2^70 (a wave holds one row)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= 0x1p-70f;
+      ms = mean_square();
+      eps *= 0x1p-140f;
+    }
+    const float inv = 1.0f / sqrtf(ms + eps);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * (float)w[i];
   }

@@ -998,3 +998,31 @@ def test_scale_of_zero(lib, dev, shape):
         assert (np.abs(_host(lse)[i] - np.log(len(v))) <= 2.0 ** -20 + (2 * k + 8) * lo.U32).all()
         bound = lo.U16 * np.abs(v.mean(0)) + (4 * k * lo.U32 + 2.0 ** -18) * np.abs(v).mean(0)
         assert lo.check(f"query {i}", _host(out)[i], v.mean(0), bound) is None
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_norm_of_large_values(lib, dev, e4m3):
+    """The norm of rows up to the largest bf16 numbers, whose squares do not fit fp32."""
+    import torch
+    rng = np.random.default_rng(71)
+    sizes = [1e3, 1e15, 1e18, 2e19, 1e20, 1e30, 1e37, 1e38]
+    kv = torch.from_numpy(np.clip(rng.standard_normal((len(sizes), 576)), -3, 3))
+    kv[:, :512] *= torch.tensor(sizes, dtype=torch.float64)[:, None]
+    kv = kv.bfloat16()
+    kvh = kv.double().numpy()
+    w, wh = _bf(rng, (512,), dev)
+    cache = Cache(rng, 16, e4m3, dev)
+    lib.latent_cache_store(kv.to(dev), _i32(range(len(sizes)), dev), cache.latent, cache.rope, scale=cache.scale, norm_weight=w,
+                           eps=1e-6)
+    latent = cache.latent.cpu()
+    for t in range(len(sizes)):
+        y = lo.normed(kvh[t, :512], wh, 1e-6)
+        slack = lo.NORM_ERROR * np.abs(y)
+        if e4m3:
+            s = float(cache.scale[t])
+            # as in the other tests of the store: half a step of the code, the norm's error, the quotient's and the product's
+            err = lo.check(f"row {t}", lo.e4m3_value(latent[t].numpy()) * s, y, np.abs(y) * 2.0 ** -4 + 2.0 ** -10 * s + slack
+                           + np.abs(y) * (lo.NORM_ERROR + 8 * lo.U32))
+        else:
+            err = lo.check(f"row {t}", latent[t].double().numpy(), y, lo.U16 * np.abs(y) * (1 + 2 * lo.NORM_ERROR) + slack)
+        assert err is None, err
