@@ -127,7 +127,7 @@ topk_status_t indexer_cache_load_paged(const int32_t* page_table, const int32_t*
  *              tokens, the scores of positions [0, L), L = seq_lens[b] - n + i + 1
  *              clamped to [0, min(width, pages_per_row * page_size)]; other entries are
  *              left as they are.  A position whose page is missing (negative, or its
- *              slot beyond num_slots) scores -inf (the weights being finite).
+ *              slot beyond num_slots) scores -inf.
  *   lens       (num_tokens,) int32 or NULL, written: L (topk_transform's seq_lens).
  * Rows from q_starts[num_requests] on are padding: their logits are left as
  * they are, and their lens are 0.  For topk_transform, a request's row of the page table

@@ -287,10 +287,16 @@ constexpr int kBufferBytes = kManyTile * kDim * 2;
 // LDS byte offset of 16-byte chunk c (0..15) of position n's bf16 row.
 __device__ __forceinline__ int tile_offset(int n, int c) { return n * (kDim * 2) + ((c ^ (n & 15)) << 4); }
 
+// A score, or -inf where the key is not there, whatever the product of nothing came to.  (A choice by bits, one
+// instruction: a comparison became a branch around the arithmetic.)
+__device__ __forceinline__ uint32_t score_bits(float score, uint32_t there) {
+  return (__float_as_uint(score) & there) | (0xFF800000u & ~there);
+}
+
 __global__ __launch_bounds__(kThreads, 2) void many_logits_kernel(PagedLogitsArgs a, uint32_t most) {
   __shared__ SharePlan plan;
   __shared__ __attribute__((aligned(16))) char buffers[2 * kBufferBytes];
-  __shared__ float2 scale_bias[2][kManyTile];
+  __shared__ uint2 scale_there[2][kManyTile];      // a key's scale, and all ones in the bits or none: is it there?
   const PagedKeys& c = a.cache;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, hb = lane >> 5;
@@ -332,7 +338,8 @@ __global__ __launch_bounds__(kThreads, 2) void many_logits_kernel(PagedLogitsArg
       const int sn = tid >> 2, sc = tid & 3;
       struct Loaded {
         uint4 r0, r1;
-        float scale, bias;
+        float scale;
+        uint32_t there;
       };
       auto key_position = [&](uint32_t tile) {
         const int32_t j = (int32_t)((tile < stop ? tile : stop - 1) * kManyTile) + sn;
@@ -345,7 +352,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_logits_kernel(PagedLogitsArg
         v.r0 = src[0];
         v.r1 = src[1];
         v.scale = *(slot >= 0 ? c.scale + slot : reinterpret_cast<const float*>(kNoKey));
-        v.bias = slot >= 0 ? 0.f : -INFINITY;
+        v.there = slot >= 0 ? 0xFFFFFFFFu : 0u;
       };
       auto stage = [&](const Loaded& v, int buf) {
         char* t = buffers + buf * kBufferBytes;
@@ -353,10 +360,10 @@ __global__ __launch_bounds__(kThreads, 2) void many_logits_kernel(PagedLogitsArg
         *reinterpret_cast<bf16x8*>(t + tile_offset(sn, 4 * sc + 1)) = widen8(v.r0.z, v.r0.w);
         *reinterpret_cast<bf16x8*>(t + tile_offset(sn, 4 * sc + 2)) = widen8(v.r1.x, v.r1.y);
         *reinterpret_cast<bf16x8*>(t + tile_offset(sn, 4 * sc + 3)) = widen8(v.r1.z, v.r1.w);
-        if (sc == 0) scale_bias[buf][sn] = make_float2(v.scale, v.bias);
+        if (sc == 0) scale_there[buf][sn] = make_uint2(__float_as_uint(v.scale), v.there);
       };
       f32x16 acc[2][kManyRows] = {};      // of the tile being multiplied, and of the one before
-      float2 sb = make_float2(0.f, 0.f);  // of the one before: scale and bias of the lane's key, and where its score goes
+      uint2 st = make_uint2(0, 0);        // of the one before: the lane's key's scale, whether it is there, and where its score goes
       uint32_t at = kDropped;
       auto multiply = [&](int buf, int half, uint32_t position, bool finish) {
         f32x16(&now)[kManyRows] = acc[half];
@@ -374,11 +381,10 @@ __global__ __launch_bounds__(kThreads, 2) void many_logits_kernel(PagedLogitsArg
         if (finish) {
 #pragma unroll
           for (int i = 0; i < kManyRows; ++i) {
-            const float score = finish_score(rows[i], before[i], sb.x, lane) + sb.y;
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(score), out[i], at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(score_bits(finish_score(rows[i], before[i], __uint_as_float(st.x), lane), st.y), out[i], at, 0, 0);
           }
         }
-        sb = scale_bias[buf][nb];
+        st = scale_there[buf][nb];
         at = hb == 0 ? position * 4 : kDropped;
       };
       Loaded l0, l1;
@@ -411,8 +417,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_logits_kernel(PagedLogitsArg
       // the last tile's scores
 #pragma unroll
       for (int i = 0; i < kManyRows; ++i) {
-        const float score = finish_score(rows[i], acc[1][i], sb.x, lane) + sb.y;
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(score), out[i], at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(score_bits(finish_score(rows[i], acc[1][i], __uint_as_float(st.x), lane), st.y), out[i], at, 0, 0);
       }
     }
     lo = begin + last;

@@ -570,3 +570,49 @@ def test_norm_of_large_values(lib, dev, mix):
     for t in range(len(sizes) - 1):
         _check_row(f"row {t}", kh[t], codes[t], s[t], weight=w.double().numpy(), bias=bias.double().numpy(), eps=1e-6, mix=mix)
     assert np.isnan(s[len(sizes) - 1])
+
+
+# ---- pages that are not there, in every form of the scores --------------------------------------
+
+@pytest.mark.parametrize("ps", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("new", [1, 2, 3, 9])
+def test_scores_of_missing_pages(lib, dev, new, ps):
+    """Negative pages and pages beyond the cache, where tokens see them: -inf whatever the weights, one token a request (of pages
+    that hold whole tiles of keys and of others), two, and more; keys that are there have their scores."""
+    import torch
+    rng = np.random.default_rng(31)
+    B, P = 7, 12
+    slots = 50 * ps - (0 if 50 * ps % 32 == 0 else 50 * ps % 32)
+    codes, sc = _finite_codes(rng, (slots, 128)), rng.uniform(0.5, 2, slots).astype(np.float32)
+    table = rng.integers(0, slots // ps, (B, P))
+    table[:, 0], table[:, 5], table[1:, 7] = -1, -2 ** 31, 10 ** 7
+    table[:, 3], table[:, 9], table[0, 7] = slots // ps, 2 ** 31 - 1, -5
+    lens = rng.integers(9 * ps + new, P * ps + 1, B)
+    lens[2], lens[3] = new, P * ps
+    q, w = _finite_codes(rng, (B * new, 32, 128)), rng.standard_normal((B * new, 32)).astype(np.float32)
+    starts = np.arange(B + 1) * new
+    d = dict(q=torch.from_numpy(q).to(dev), w=torch.from_numpy(w).to(dev), k=torch.from_numpy(codes).to(dev),
+             s=torch.from_numpy(sc).to(dev), t=_i32(table, dev), n=_i32(lens, dev), b=_i32(starts, dev))
+    wild = d["w"].clone()
+    wild[:, 3], wild[:, 4], wild[::2, 5] = float("inf"), float("-inf"), float("nan")
+    note(f"missing pages new={new} ps={ps}")
+    got, rows = lib.indexer_logits_paged(d["q"], d["w"], d["k"], d["s"], d["t"], d["n"], d["b"], ps)
+    other, _ = lib.indexer_logits_paged(d["q"], wild, d["k"], d["s"], d["t"], d["n"], d["b"], ps)
+    got, other, seen = got.cpu().numpy(), other.cpu().numpy(), {"negative": 0, "beyond": 0}
+    for b in range(B):
+        for i in range(new):
+            t, L = b * new + i, int(lens[b]) - new + i + 1
+            assert int(rows[t]) == L
+            pos = np.arange(L)
+            page = table[b].astype(np.int64)[pos // ps]
+            slot = page * ps + pos % ps
+            ok = (page >= 0) & (slot < slots)
+            seen["negative"] += int((page < 0).any())
+            seen["beyond"] += int((slot >= slots).any())
+            slot = np.where(ok, slot, 0)
+            row = codes[slot], sc[slot]
+            want = np.where(ok, ix.indexer_scores_row(q[t], w[t], *row, range(L)), -np.inf)
+            err = check(f"{b} {i}", got[t, :L], want, ix.fp32_error_bound(q[t], w[t], *row, range(L)))
+            assert err is None, err
+            assert np.isneginf(other[t, :L][~ok]).all() and not np.isfinite(other[t, :L]).any()
+    assert min(seen.values()) >= (B - 1) * new
