@@ -616,3 +616,84 @@ def test_scores_of_missing_pages(lib, dev, new, ps):
             assert err is None, err
             assert np.isneginf(other[t, :L][~ok]).all() and not np.isfinite(other[t, :L]).any()
     assert min(seen.values()) >= (B - 1) * new
+
+
+# ---- many tiles to a workgroup, many requests to a workgroup ------------------------------------
+
+LONG = {
+    # cached lengths, new tokens: enough for several tiles (of 128 keys, with three tokens or more 64) to each of the workgroups, of
+    # which there are four or two a CU; or for several requests to each
+    "one_token": ([1_000_003], [1]),
+    "two_tokens": ([700_001], [2]),
+    "decode": ([3 + (i * 7919) % 65536 for i in range(64)], [1] * 64),
+    "two_each": ([3 + (i * 7919) % 65536 for i in range(64)], [2] * 64),
+    "chunk": ([16_391], [1003]),
+    "chunks": ([9_000, 20_001, 70, 12_345], [300, 129, 70, 517]),
+    "three_each": ([3 + (i * 7919) % 33333 for i in range(40)], [3] * 40),
+    "short": ([1 + (i * 37) % 300 for i in range(3000)], [1] * 3000),
+    "short_two_each": ([2 + (i * 37) % 300 for i in range(2000)], [2] * 2000),
+    "short_some": ([9 + (i * 37) % 300 for i in range(1500)], [(i * 5) % 9 for i in range(1500)]),
+    "mixed": ([40_000] + [2000 + (i * 7919) % 9000 for i in range(63)], [1500] + [1] * 63),
+}
+
+
+@pytest.mark.parametrize("ps", [8, 64])
+@pytest.mark.parametrize("name", sorted(LONG))
+def test_scores_of_long_shares(lib, dev, name, ps):
+    """Loops that run many times in each workgroup and pass from request to request: every score is, bit by bit, that of
+    the scan over the same keys in a row, and some are held against the oracle."""
+    import torch
+    lens, new = LONG[name]
+    B, T, P = len(lens), sum(new), -(-max(lens) // ps)
+    gen = torch.Generator(device=dev).manual_seed(sorted(LONG).index(name))
+    pages = -(-np.asarray(lens) // ps)
+    total = int(pages.sum())
+    slots = (total + 8) // 8 * 8 * ps                     # a multiple of 32 or more
+    keys = torch.randint(0, 256, (slots, 128), dtype=torch.uint8, device=dev, generator=gen)
+    keys = torch.where((keys & 0x7F) == 0x7F, keys ^ 0x10, keys)
+    scale = torch.rand(slots, device=dev, generator=gen) + 0.5
+    q = torch.randint(0, 256, (T, 32, 128), dtype=torch.uint8, device=dev, generator=gen)
+    q = torch.where((q & 0x7F) == 0x7F, q ^ 0x10, q)
+    w = torch.randn((T, 32), device=dev, generator=gen)
+    rng = np.random.default_rng(7)
+    order, table, at = rng.permutation(total), np.full((B, P), -1, np.int64), 0
+    for b in range(B):
+        table[b, :pages[b]] = order[at:at + pages[b]]
+        at += pages[b]
+    for b, page in ((0, -3), (B - 1, 10 ** 7), (B // 2, -1)):
+        table[b, pages[b] // 2] = page                    # not there, within what tokens see
+    tab, n, starts = _i32(table, dev), _i32(lens, dev), np.concatenate([[0], np.cumsum(new)])
+    width = P * ps
+    out = torch.full((T, width), float(GUARD), device=dev)
+    note(f"long shares {name} ps={ps} T={T} width={width}")
+    got, rows = lib.indexer_logits_paged(q, w, keys, scale, tab, n, _i32(starts, dev), ps, out=out)
+    want_rows = np.concatenate([[lens[b] - new[b] + i + 1 for i in range(new[b])] for b in range(B)]).clip(0)
+    np.testing.assert_array_equal(rows.cpu().numpy(), want_rows)
+    # the keys in a row, and which of them are there
+    kv = np.concatenate([[0], np.cumsum(lens)])
+    flat, fscale = lib.indexer_cache_load_paged(tab, _i32(kv, dev), ps, int(kv[-1]), keys, scale)
+    first = torch.from_numpy(np.repeat(kv[:-1], new)).to(dev)
+    ks, ke = first.int(), (first + rows).int()
+    want = lib.indexer_logits(q, w, flat, fscale, ks, ke, width)
+    owner = torch.from_numpy(np.repeat(np.arange(B), new)).to(dev)
+    there = (tab >= 0) & (tab < slots // ps)
+    for t0 in range(0, T, 512):                           # some rows at a time
+        t = slice(t0, min(T, t0 + 512))
+        inside = torch.arange(width, device=dev)[None, :] < rows[t, None]
+        ok = there[owner[t]].repeat_interleave(ps, 1)
+        full = torch.where(inside, torch.where(ok, want[t], float("-inf")), float(GUARD))
+        same = got[t] == full
+        assert bool(same.all()), [x[:4].tolist() for x in torch.nonzero(~same, as_tuple=True)]
+    for t in rng.integers(0, T, 6):
+        L, b = int(want_rows[t]), int(owner[t])
+        if L == 0:
+            continue
+        pos = np.unique(np.concatenate([[0, L - 1], rng.integers(0, L, 200)]))
+        page = table[b][pos // ps]
+        slot = np.where((page >= 0) & (page < slots // ps), page * ps + pos % ps, -1)
+        pos, slot = pos[slot >= 0], slot[slot >= 0]
+        row = keys.cpu().numpy()[slot], scale.cpu().numpy()[slot]
+        qt, wt = q[t].cpu().numpy(), w[t].cpu().numpy()
+        err = check(f"token {t}", got[t].cpu().numpy()[pos], ix.indexer_scores_row(qt, wt, *row, range(len(pos))),
+                    ix.fp32_error_bound(qt, wt, *row, range(len(pos))))
+        assert err is None, err
