@@ -432,3 +432,40 @@ def test_a_score_of_minus_infinity_weighs_nothing(lib, dev, e4m3, name):
     k = int(x.starts[-1])
     assert torch.equal(torch.isnan(a[:k]), torch.isnan(w[:k])) and torch.equal(torch.isnan(al[:k]), torch.isnan(wl[:k]))
     assert bool(torch.isnan(a[:k]).any())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,new,H,prefix,own", [(64, 1, 32, 7000, 900), (40, 3, 20, 12001, 333), (300, 1, 16, 2050, 60), (5, 2, 128, 20000, 4000)])
+def test_many_tiles_to_a_workgroup(lib, dev, e4m3, B, new, H, prefix, own):
+    """Parts of some tens of tiles, where the other cases have six at most: all tokens within the roundings of the call over
+    whole sequences, which reads every request's own copy of the same page table, and some against the oracle."""
+    import torch
+    rng = np.random.default_rng(B)
+    ps = 16
+    lens = prefix + rng.integers(new, own + 1, B)
+    shared = prefix // ps * ps
+    pages = -(-lens // ps) - shared // ps
+    total, P = shared // ps + int(pages.sum()), int((shared // ps + pages).max())
+    order, at = rng.permutation(total), shared // ps
+    table = np.full((B, P), -1, np.int64)
+    for b in range(B):
+        table[b, :shared // ps] = order[:shared // ps]
+        table[b, shared // ps:shared // ps + pages[b]] = order[at:at + pages[b]]
+        at += pages[b]
+    cache = Cache(rng, total * ps, e4m3, dev)
+    T = B * new
+    q, qh = _bf(rng, (T, H, 576), dev)
+    args = (q, cache.latent, cache.rope, _i32(table, dev), _i32(lens, dev), _i32(np.arange(B + 1) * new, dev))
+    note(f"long parts e4m3={e4m3} B={B} H={H}")
+    out, lse = lib.latent_attention_shared(*args, _i32([0, B], dev), _i32([shared], dev), ps, 0.06, scale=cache.scale)
+    want, wlse = lib.latent_attention_paged(*args, ps, 0.06, scale=cache.scale)
+    # a bf16 result's own rounding, and its weights', on either side (2^-8 each, of the row's largest element)
+    size = want.float().abs().amax(-1, keepdim=True)
+    assert bool(((out.float() - want.float()).abs() <= 4 * 2.0 ** -8 * size).all())
+    assert bool(((lse - wlse).abs() <= 1e-5 * (1 + wlse.abs())).all())
+    out, lse = _host(out), _host(lse)
+    for b in sorted({0, B // 2, B - 1}):
+        i = int(rng.integers(new))
+        pos = np.arange(int(lens[b]) - new + i + 1)
+        _check_token(f"request {b} token {i}", cache, qh[b * new + i], table[b][pos // ps] * ps + pos % ps, 0.06,
+                     out[b * new + i], lse[b * new + i], (0, H // 2, H - 1))
