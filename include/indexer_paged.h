@@ -24,7 +24,7 @@
  *   scale = max|y| / 448, but 2^-126 at least (1 where y is all zero), codes = y / scale, a quotient in
  *     fp32 (with mixing, of numerator and denominator without their factor 1 / sqrt(128)), rounded to
  *     nearest even.  A row with a NaN or an infinity has a NaN scale, and so has one whose sums in the
- *     mixing leave fp32 (values beyond 2^120).
+ *     rotation or the mixing leave fp32 (values beyond 2^120).
  * cos_sin (max_positions, 64) fp32: the cosines of the 32 angles of a position, then
  * their sines; 16-byte aligned.  All arithmetic is fp32; each stored value is rounded once.
  *
@@ -133,6 +133,9 @@ topk_status_t indexer_cache_load_paged(const int32_t* page_table, const int32_t*
  * they are, and their lens are 0.  For topk_transform, a request's row of the page table
  * stands for each of its tokens.
  * num_tokens * (width / 64 + 1) must stay below 2^31, and width below 2^29.
+ * Results do not depend on what else is in a call, but its time does: how many tokens a key is read for at once
+ * follows num_tokens / num_requests (requests without new tokens and padding among them), so a long chunk and many
+ * requests of one token, or of none, are faster in calls of their own.
  */
 topk_status_t indexer_logits_paged(const uint8_t* q, const float* weights, const uint8_t* keys, int64_t key_stride,
                                    const float* key_scale, const int32_t* page_table, const int32_t* seq_lens,

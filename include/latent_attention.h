@@ -113,7 +113,7 @@ topk_status_t paged_append_plan(const int32_t* kv_lens, const int32_t* new_lens,
  *   slot_map    (num_tokens,) int32.  Tokens with a slot outside [0, num_slots), or
  *               (with cos_sin) a position outside [0, max_positions), are not
  *               stored.  No two tokens may name one slot (parts of either would be stored).
- * E4M3 caches: scale[slot] = max|y| / 448 (1 where y is all zero), codes =
+ * E4M3 caches: scale[slot] = max|y| / 448, but 2^-126 at least (1 where y is all zero), codes =
  * y / scale rounded to nearest even.  A row whose y has a NaN or an infinity
  * reads back as NaN throughout (its scale is NaN).  All arithmetic
  * is fp32; each stored value is rounded once.

@@ -219,7 +219,9 @@ __device__ __forceinline__ bf16x8 weights_of_tile(HeadState& st, f32x4 (&s)[2], 
     }
   }
   // Weights in bf16 (the matrix cores' type): an unbiased rounding of at most 2^-8 on
-  // each, as large as the rounding of the result itself.  The sum keeps them in fp32.
+  // each (over codes of the weight times the key's scale, as one), as large as the rounding of the
+  // result itself: against 64 bits results are off by 0.0017 to 0.0022 (relative, in the mean square), with fp32
+  // weights by 0.0017.  Two bf16 terms a weight would double the second product.  The sum keeps them in fp32.
   bf16x8 p;
   float sum = 0.f;                        // a tile at a time: few additions to a large number
 #pragma unroll

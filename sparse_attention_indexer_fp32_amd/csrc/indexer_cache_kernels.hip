@@ -2,7 +2,7 @@
 // their paged cache, the queries in the same form, and cached keys laid in a row.
 //
 // Each value is read and each code written once, and memory bounds all three (MI355X, host included):
-// the queries of 8192 tokens 23.5 us, 4.5 TB/s read and written, where a large copy reaches 5.1; the load
+// the queries of 8192 tokens 22.5-25 us, 4.2-4.7 TB/s read and written, where a large copy reaches 5.1; the load
 // of 400000 rows 20.5 us, 5.1 TB/s; the store of 16000 keys 8.3 us and every smaller call as much,
 // which is the host's part of a launch.
 

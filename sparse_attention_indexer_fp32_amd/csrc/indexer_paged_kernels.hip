@@ -13,7 +13,7 @@
 //
 // Measured (MI355X), 64-position pages: one token of each of 64 requests behind 4096 to 65536 keys
 // 56-60 us, 5.1-5.4 TB/s (a loop that only reads the same bytes: 44-50); one token behind 2^20 keys 26
-// us, 5.4 TB/s; 1024 tokens behind 65536 keys 447-490 us, 1130-1230 TFLOP/s, which is what a large
+// us, 5.4 TB/s; 1024 tokens behind 65536 keys 447-496 us, 1110-1230 TFLOP/s, which is what a large
 // library matrix product reaches less 10-20 %.
 
 #include <hip/hip_runtime.h>
@@ -449,6 +449,10 @@ hipError_t launch_paged_logits(const PagedLogitsArgs& a, int cus, hipStream_t st
   //   many                          95     92    114    114    150
   // (with three tokens the last two are within a sixth of each other elsewhere: 16 such requests 28 and 34, one
   // behind a million keys 57 and 60, 200 behind 1000 to 20000 118 and 114)
+  // The average is all that the host knows.  Where it misleads: 512 tokens of one request and one of each of 63
+  // others 252 us (137 and 54 in calls of their own); 64 tokens of one beside 63 requests without any 33 (alone 29), 1000
+  // behind 16384 keys beside 999 short ones without any 231 (alone 124); 512 and one each of 511, behind 4096 keys, 78
+  // (77 in two calls).
   const int64_t tokens = a.num_tokens, requests = a.cache.num_requests;
   const int form = tokens <= requests ? 1 : (tokens <= 2 * requests ? 2 : 3);
   const int64_t tiles = tokens * (a.most_keys / (form < 3 ? kFewTile : kManyTile) + 1), most = (form == 1 ? 4 : 2) * (int64_t)cus;

@@ -22,9 +22,10 @@
 // instructions: 245.)
 //
 // Measured (MI355X): 64 requests x 32 heads behind 32768 positions 203 us + 15 of the join, up to 725
-// TFLOP/s: matrix instructions, vector instructions and LDS are busy for 44 to 47 % of the time each,
+// TFLOP/s: matrix instructions, vector instructions and LDS are busy for 43 to 48 % of the time each,
 // and 15 % is waiting for rows (with one row for all, from L1: 181).  8 x 16 behind 4096 20 + 5 us.
-// 150 x 2 tokens x 20 heads over codes 225-237 us: vector instructions, 68 %.
+// 150 x 2 tokens x 20 heads over codes 225-237 us: vector instructions, 70 %.  (All 256 vector registers are in use; 12 of
+// bf16 and 18 over codes are spilled around the parts, none is reloaded in the loop over the tiles.)
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
